@@ -447,6 +447,156 @@ SWA_API int swa_ring_slot_positions(int B, const int64_t *n_written, int64_t W, 
                             void *stream);
 
 /*
+ * A cache in pages shared by all sequences, and the table that maps positions
+ * to pages.  Passage: M003 note section 06 (logical positions against physical
+ * slots); blog section 3.2 (the cache of a windowed layer).
+ *   Position p of sequence b lives in page table[b * table_stride +
+ *   p / page_size], slot p % page_size.  The key of head h there is the d
+ *   elements at k + page * page_stride + h * head_stride + slot * slot_stride,
+ *   the value the same of v (strides in elements, shared by k and v, so both
+ *   [n_pages, Hkv, page_size, d] and [n_pages, page_size, Hkv, d] caches work).
+ *   k, v: bf16, device, 16-byte aligned; strides: positive multiples of 8,
+ *      page_stride < 2^39; distinct (page, head, slot) rows must not overlap.
+ *   table: int32, device; only the entries of pages that hold a slot visible
+ *      to a query of the call (append: a slot it writes) are read, so those of
+ *      pages that were given back (behind the window and the sinks) may hold
+ *      anything.
+ *   page_size: a multiple of 8, up to 65536;  1 <= n_pages < 2^31 - 1;
+ *      max_pages: entries per sequence (<= table_stride),
+ *      max_pages * page_size < 2^31 - 1024.
+ * The struct is read during the call only.
+ */
+typedef struct swa_paged_cache {
+  void *k;
+  void *v;
+  const int32_t *table;
+  int64_t page_stride, head_stride, slot_stride;
+  int64_t n_pages, max_pages, table_stride;
+  int32_t page_size;
+} swa_paged_cache;
+
+/*
+ * The position rotation that swa_paged_append applies to keys and queries.
+ * The pages have no counterpart: their models rotate before the attention.
+ *   Pair i (0 <= i < rot_dim / 2) of a head is elements (i, i + rot_dim / 2),
+ *   or (2i, 2i + 1) when interleaved != 0; it turns by the angle
+ *   position * inv_freq[i]:  (x, y) -> (x cos - y sin, y cos + x sin).
+ *   Elements rot_dim .. d-1 pass through.  The angle is reduced in 64 bits,
+ *   so far positions keep the accuracy of near ones.
+ *   inv_freq: fp32 [rot_dim / 2], device;  rot_dim: a multiple of 16, <= d.
+ *   positions: int64 [n_axes, total], device, rows positions_stride apart, or
+ *      NULL: every pair uses the token's position in its sequence.
+ *   pair_axis: int32 [rot_dim / 2], device: the row of positions that pair i
+ *      uses (time, height, width of an image token, say), or NULL: row 0 for
+ *      every pair.  An entry outside 0 .. n_axes-1 sets SWA_ERR_DEVICE on the
+ *      device and counts as 0.
+ */
+typedef struct swa_rotation {
+  const float *inv_freq;
+  const int64_t *positions;
+  const int32_t *pair_axis;
+  int64_t positions_stride;
+  int32_t rot_dim, interleaved, n_axes;
+} swa_rotation;
+
+/*
+ * swa_paged_append -- append the keys and values of new tokens to a paged
+ * cache, with the position rotation applied on the way.
+ * Passage: M003 note section 06 (update the position-to-slot map, then write);
+ * blog section 3.2.  The paged counterpart of swa_ring_write.
+ *   k_new, v_new: [total, Hkv, d] bf16, device, token rows k_new_stride and
+ *      v_new_stride elements apart (views of one fused projection work);
+ *   q, q_out: [total, H, d] bf16, device, token rows q_stride and q_out_stride
+ *      apart: the queries of the same tokens, rotated like the keys and
+ *      written to q_out (q_out == q with equal strides rotates in place); or
+ *      both NULL.  Strides: multiples of 8, at least heads * d.
+ *   cu_seqlens: int64 [n_seq + 1], device: sequence b is tokens cu_seqlens[b]
+ *      .. cu_seqlens[b+1] - 1, non-decreasing, cu_seqlens[n_seq] <= total.
+ *   q_start: int64 [n_seq], device: the position of its first new token.
+ *   rotation: NULL: none (queries are copied).
+ *   zero_rest: q_out rows of tokens that write no slot are left as they were
+ *      (0) or set to zero (1).
+ * Token t of sequence b goes to position q_start[b] + t - cu_seqlens[b].
+ * Tokens outside every sequence write no slot.
+ * SWA_ERR_DEVICE is set on the device, and the token writes no slot, for
+ * offsets out of order or range, a negative start, a position past
+ * max_pages * page_size, or a table entry outside 0 .. n_pages-1.
+ * Limits: 1 <= total < 2^31 - 256, n_seq < 2^24, d in {64, 128}; two tokens of
+ * one call must not share a slot.
+ */
+SWA_API int swa_paged_append(const void *k_new, int64_t k_new_stride, const void *v_new,
+                             int64_t v_new_stride, const void *q, int64_t q_stride, void *q_out,
+                             int64_t q_out_stride, const swa_paged_cache *cache,
+                             const swa_rotation *rotation, const int64_t *cu_seqlens,
+                             const int64_t *q_start, int n_seq, int64_t total, int H, int Hkv,
+                             int d, int zero_rest, void *stream);
+
+/*
+ * swa_chunk_paged_workspace_bytes, swa_decode_paged_workspace_bytes -- bytes
+ * of scratch swa_attn_chunk_paged and swa_attn_decode_paged need for these
+ * sizes on the current device (its SM count sets how far they split), a
+ * multiple of 256; 0 for invalid sizes.
+ */
+SWA_API size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d);
+SWA_API size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d);
+
+/*
+ * swa_attn_chunk_paged -- attention of new tokens over a paged cache.
+ * Passage: Chapter 10 section 10.2 (a chunk attends to the cache and to
+ * itself); M003 note section 06; blog section 5.2 tip 4 (windows per
+ * sequence); taxonomy page section 3.2 for the sinks.  The paged counterpart
+ * of swa_attn_chunk_ring, for packed ragged batches.
+ *   q: [total, H, d] bf16, device, packed as swa_paged_append's tokens;
+ *   cu_seqlens, q_start: as swa_paged_append.  Query t of sequence b sits at
+ *      p = q_start[b] + t and reads key j iff j <= p and (j >= p - W + 1 or
+ *      j < n_sink).  All visible positions, the new tokens' own among them,
+ *      must be in the cache before the call.
+ *   out: [total, H, d] bf16, device;  lse: [H, total] fp32, device, or NULL.
+ *   zero_rest: rows of tokens before cu_seqlens[0] and from cu_seqlens[n_seq]
+ *      on are left as they were (0), or set to zero in out and lse (1).
+ *   workspace: at least swa_chunk_paged_workspace_bytes(...) bytes, 256-byte
+ *      aligned, caller-owned, contents on entry ignored; two calls in flight
+ *      at once need workspaces of their own.
+ * Values of visible slots must be finite; slots that no query of the call may
+ * see can hold anything, NaN and infinities included.
+ * SWA_ERR_DEVICE is set on the device for a sequence with offsets out of order
+ * or range, a negative start or an end past max_pages * page_size (it is
+ * skipped, its rows not written), and for a visible page whose table entry is
+ * outside 0 .. n_pages-1 (its keys and values count as zeros).
+ * Limits: 1 <= total < 2^31 - 256, n_seq < 2^24, H / Hkv <= 128, d in
+ * {64, 128}, 0 <= n_sink <= 128, W >= 1 (W past the longest sequence: plain
+ * causal attention).
+ */
+SWA_API int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache,
+                                 const int64_t *cu_seqlens, const int64_t *q_start, void *out,
+                                 float *lse, int n_seq, int64_t total, int H, int Hkv, int d,
+                                 int64_t W, int n_sink, float scale, int zero_rest,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * swa_attn_decode_paged -- batched single-token decode over a paged cache.
+ * Passage: blog section 3.2; taxonomy page sections 1 (a decode step is bound
+ * by reading the cache) and 3.2 (sinks).  The paged counterpart of
+ * swa_attn_decode_ring, without a limit on H / Hkv.
+ *   q: [B, H, d] bf16, device: the query of sequence b at position pos[b],
+ *      whose own key and value are in the cache; it reads key j iff
+ *      j <= pos[b] and (j >= pos[b] - W + 1 or j < n_sink).
+ *   pos: int64 [B], device.  pos[b] == -1 marks a padded row that sees
+ *      nothing: its output is zero and its lse -infinity.  Other negative
+ *      values and positions past max_pages * page_size set SWA_ERR_DEVICE on
+ *      the device and count as -1.
+ *   out: [B, H, d] bf16, device;  lse: [B, H] fp32, device, or NULL.
+ *   workspace: at least swa_decode_paged_workspace_bytes(...) bytes, as
+ *      swa_attn_chunk_paged.
+ * Finite values, table entries out of range, n_sink and W: as
+ * swa_attn_chunk_paged.  Limits: B < 2^24, B * H <= 2^24, d in {64, 128}.
+ */
+SWA_API int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int64_t *pos,
+                                  void *out, float *lse, int B, int H, int Hkv, int d, int64_t W,
+                                  int n_sink, float scale, void *workspace,
+                                  size_t workspace_bytes, void *stream);
+
+/*
  * swa_selftest_wait -- runs the bounded device wait that every kernel of
  * this library uses for failure detection, in a one-CTA kernel of its own
  * (no copies, no tensor memory), so that the timeout path can be checked

@@ -13,16 +13,20 @@ key/value rows before each shard and then calls ``swa_ring_write`` and
 
 Layouts (row-major bf16): queries ``[B, H, rows, d]``, keys/values
 ``[B, Hkv, rows, d]``, ring caches ``[B, Hkv, W, d]``; query head h reads
-key/value head ``h // (H // Hkv)``.
+key/value head ``h // (H // Hkv)``.  Paged caches are ``[n_pages, Hkv,
+page_size, d]`` tensors of any strides (a token-major cache is passed as
+``cache.transpose(1, 2)``) with an int32 page table ``[n_seq, max_pages]``.
 """
 
 from __future__ import annotations
 
+import contextlib
+import ctypes
 import math
 
 import torch
 
-from ._native import SwaError, check, lib, status_name  # noqa: F401
+from ._native import PagedCache, Rotation, SwaError, check, lib, status_name  # noqa: F401
 
 __all__ = [
     "SwaError",
@@ -44,6 +48,11 @@ __all__ = [
     "swa_attn_decode_ring_sink",
     "swa_attn_decode_ring_static",
     "swa_ring_slot_positions",
+    "swa_paged_append",
+    "swa_chunk_paged_workspace_bytes",
+    "swa_attn_chunk_paged",
+    "swa_decode_paged_workspace_bytes",
+    "swa_attn_decode_paged",
     "swa_selftest_wait",
     "swa_get_device_status",
     "swa_version",
@@ -449,6 +458,226 @@ def swa_ring_slot_positions(n_written, W: int, out=None):
     check("swa_ring_slot_positions", lib().swa_ring_slot_positions(
         B, _ptr(n_written), W, _ptr(out), _stream(n_written.device)))
     return out
+
+
+def _one_device(first, **others):
+    """All tensors on one CUDA device; a context in which it is the current one."""
+    dev = first.device
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return (contextlib.nullcontext() if torch.cuda.current_device() == dev.index
+            else torch.cuda.device(dev))
+
+
+def _need_rows(t, name, shape):
+    """bf16 [tokens, heads, d] whose token rows may lie apart (a slice of a fused projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor of shape {list(shape)}, got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    heads, d = shape[1:]
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must hold each token's [heads, d] contiguously")
+    return t.stride(0) if shape[0] > 1 else heads * d
+
+
+def _need_int(t, name, dtype, shape):
+    _need(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _paged_cache(k_cache, v_cache, block_table, n_seq, Hkv, d):
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{n} must be a torch.Tensor")
+        if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4:
+            raise ValueError(f"{n} must be a bfloat16 CUDA tensor [n_pages, Hkv, page_size, d]")
+        if t.stride(3) != 1:
+            raise ValueError(f"{n} must be contiguous in its last dimension")
+    n_pages, heads, page_size, dk = k_cache.shape
+    # the stride of a dimension of one entry says nothing: any valid one will do
+    strides = [k_cache.stride(i) if k_cache.shape[i] > 1 else dk for i in range(3)]
+    if v_cache.shape != k_cache.shape or \
+            [v_cache.stride(i) if v_cache.shape[i] > 1 else dk for i in range(3)] != strides:
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    if heads != Hkv or dk != d:
+        raise ValueError(f"the cache has {heads} heads of {dk}, expected {Hkv} of {d}")
+    if not isinstance(block_table, torch.Tensor):
+        raise TypeError("block_table must be a torch.Tensor")
+    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            block_table.shape[0] != n_seq or (block_table.shape[1] > 1 and
+                                              block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be an int32 CUDA tensor [{n_seq}, max_pages], "
+                         "contiguous along a row")
+    max_pages = block_table.shape[1]
+    return PagedCache(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), strides[0], strides[1],
+                      strides[2], n_pages, max_pages,
+                      block_table.stride(0) if n_seq > 1 else max_pages, page_size)
+
+
+def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_start, q=None,
+                     q_out=None, inv_freq=None, interleaved: bool = False, positions=None,
+                     pair_axis=None):
+    """Append packed new tokens to a paged cache, rotating keys (and queries) on the way.
+
+    k_new, v_new [total, Hkv, d] (rows may lie apart, as in a slice of a fused projection) go to
+    the pages of their sequences: token t of sequence b (cu_seqlens int64 [n_seq + 1]) to position
+    q_start[b] + t - cu_seqlens[b], page block_table[b, position // page_size].  inv_freq float32
+    [rot_dim / 2] turns the first rot_dim elements of every key and query head by position *
+    inv_freq[i], in pairs (i, i + rot_dim / 2) or, when interleaved, (2i, 2i + 1); positions
+    int64 [total] or [n_axes, total] and pair_axis int32 [rot_dim / 2] give each pair a position
+    of its own (time, height, width).  Returns the rotated queries: q_out, a new tensor when None
+    (zeros where a token writes no slot), or None when q is None.  q_out may be q itself.
+    """
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
+        raise ValueError("k_new must be [total, Hkv, d]")
+    total, Hkv, d = k_new.shape
+    ks = _need_rows(k_new, "k_new", (total, Hkv, d))
+    vs = _need_rows(v_new, "v_new", (total, Hkv, d))
+    _need(cu_seqlens, "cu_seqlens", torch.int64, 1)
+    n_seq = cu_seqlens.shape[0] - 1
+    _need_int(q_start, "q_start", torch.int64, (n_seq,))
+    cache = _paged_cache(k_cache, v_cache, block_table, n_seq, Hkv, d)
+    H, qs, qos, zero_rest = 0, 0, 0, False
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be [total, H, d]")
+        H = q.shape[1]
+        qs = _need_rows(q, "q", (total, H, d))
+        zero_rest = q_out is None
+        if zero_rest:
+            q_out = torch.empty((total, H, d), dtype=q.dtype, device=q.device)
+        qos = _need_rows(q_out, "q_out", (total, H, d))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rotation = None
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, 1)
+        half = inv_freq.shape[0]
+        n_axes = 0
+        if positions is not None:
+            _need(positions, "positions", torch.int64)
+            if positions.dim() not in (1, 2) or positions.shape[-1] != total:
+                raise ValueError(f"positions must be [{total}] or [n_axes, {total}]")
+            n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        if pair_axis is not None:
+            if positions is None:
+                raise ValueError("pair_axis without positions")
+            _need_int(pair_axis, "pair_axis", torch.int32, (half,))
+        rotation = Rotation(_ptr(inv_freq), _ptr(positions), _ptr(pair_axis), total, 2 * half,
+                            1 if interleaved else 0, n_axes)
+    elif positions is not None or pair_axis is not None:
+        raise ValueError("positions and pair_axis need inv_freq")
+    with _one_device(k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
+                     block_table=block_table, cu_seqlens=cu_seqlens, q_start=q_start, q=q,
+                     q_out=q_out, inv_freq=inv_freq, positions=positions, pair_axis=pair_axis):
+        check("swa_paged_append",
+              lib().swa_paged_append(_ptr(k_new), ks, _ptr(v_new), vs, _ptr(q), qs, _ptr(q_out),
+                                     qos, ctypes.byref(cache),
+                                     ctypes.byref(rotation) if rotation else None,
+                                     _ptr(cu_seqlens), _ptr(q_start), n_seq, total, H, Hkv, d,
+                                     1 if zero_rest else 0, _stream(k_new.device)))
+    return q_out
+
+
+def swa_chunk_paged_workspace_bytes(n_seq: int, total: int, H: int, Hkv: int, d: int) -> int:
+    return int(lib().swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d))
+
+
+def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, W: int,
+                         scale: float | None = None, n_sink: int = 0, out=None, lse=None,
+                         return_lse: bool = False, workspace=None):
+    """Attention of packed new tokens q [total, H, d] over a paged cache -> out [total, H, d].
+
+    Query t of sequence b (cu_seqlens int64 [n_seq + 1]) sits at p = q_start[b] + t and reads the
+    cached keys j <= p of its own sequence with j >= p - W + 1 or j < n_sink (its own key and
+    those of the chunk are in the cache already, see swa_paged_append).  lse is [H, total].  Rows
+    of tokens outside every sequence keep what out and lse held (zeros when allocated here).
+    """
+    _need(q, "q", dims=3)
+    _need(cu_seqlens, "cu_seqlens", torch.int64, 1)
+    total, H, d = q.shape
+    n_seq = cu_seqlens.shape[0] - 1
+    _need_int(q_start, "q_start", torch.int64, (n_seq,))
+    Hkv = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
+    cache = _paged_cache(k_cache, v_cache, block_table, n_seq, Hkv, d)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    new_out, new_lse = out is None, return_lse and lse is None
+    if out is not None:
+        _need(out, "out", dims=3)
+        if out.shape != q.shape:
+            raise ValueError("out must match q")
+    if lse is not None:
+        _need_int(lse, "lse", torch.float32, (H, total))
+    with _one_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                     cu_seqlens=cu_seqlens, q_start=q_start, out=out, lse=lse,
+                     workspace=workspace):
+        # what is allocated here is zeroed by the call outside the sequences, unless the other
+        # of the two is the caller's: then its rows stay, and ours are zeroed first
+        zero_rest = new_out and (new_lse or lse is None)
+        make = torch.empty if zero_rest else torch.zeros
+        if new_out:
+            out = make(q.shape, dtype=q.dtype, device=q.device)
+        if new_lse:
+            lse = make((H, total), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        check("swa_attn_chunk_paged",
+              lib().swa_attn_chunk_paged(_ptr(q), ctypes.byref(cache), _ptr(cu_seqlens),
+                                         _ptr(q_start), _ptr(out), _ptr(lse), n_seq, total, H, Hkv,
+                                         d, W, n_sink, scale, 1 if zero_rest else 0,
+                                         _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(),
+                                         _stream(q.device)))
+    return (out, lse) if return_lse else out
+
+
+def swa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int) -> int:
+    return int(lib().swa_decode_paged_workspace_bytes(B, H, Hkv, d))
+
+
+def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
+                          scale: float | None = None, n_sink: int = 0, workspace=None, out=None,
+                          lse=None, return_lse: bool = False):
+    """Decode over a paged cache: q [B, H, d] at positions pos [B] -> out [B, H, d], lse [B, H].
+
+    The query of sequence b reads the cached keys j <= pos[b] with j >= pos[b] - W + 1 or
+    j < n_sink.  pos[b] = -1 marks a padded row: output zero, lse -infinity.
+    """
+    _need(q, "q", dims=3)
+    B, H, d = q.shape
+    _need_int(pos, "pos", torch.int64, (B,))
+    Hkv = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
+    cache = _paged_cache(k_cache, v_cache, block_table, B, Hkv, d)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is not None:
+        _need(out, "out", dims=3)
+        if out.shape != q.shape:
+            raise ValueError("out must match q")
+    if lse is not None:
+        _need_int(lse, "lse", torch.float32, (B, H))
+    with _one_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, pos=pos,
+                     out=out, lse=lse, workspace=workspace):
+        if out is None:
+            out = torch.empty_like(q)
+        if return_lse and lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = swa_decode_paged_workspace_bytes(B, H, Hkv, d)
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        check("swa_attn_decode_paged",
+              lib().swa_attn_decode_paged(_ptr(q), ctypes.byref(cache), _ptr(pos), _ptr(out),
+                                          _ptr(lse), B, H, Hkv, d, W, n_sink, scale,
+                                          _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(),
+                                          _stream(q.device)))
+    return (out, lse) if return_lse else out
 
 
 def swa_selftest_wait(limit_ns: int, arrive: bool = False, device=None):

@@ -19,6 +19,24 @@ _f = ctypes.c_float
 _p = ctypes.c_void_p
 _sz = ctypes.c_size_t
 
+
+
+class PagedCache(ctypes.Structure):
+    """swa_paged_cache of include/swa.h."""
+
+    _fields_ = [("k", _p), ("v", _p), ("table", _p), ("page_stride", _i64), ("head_stride", _i64),
+                ("slot_stride", _i64), ("n_pages", _i64), ("max_pages", _i64),
+                ("table_stride", _i64), ("page_size", ctypes.c_int32)]
+
+
+class Rotation(ctypes.Structure):
+    """swa_rotation of include/swa.h."""
+
+    _fields_ = [("inv_freq", _p), ("positions", _p), ("pair_axis", _p),
+                ("positions_stride", _i64), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32)]
+
+
 # name -> (restype, argtypes), mirroring include/swa.h
 SIGNATURES = {
     "swa_status_string": (ctypes.c_char_p, [_i]),
@@ -51,6 +69,13 @@ SIGNATURES = {
     "swa_decode_workspace_bytes": (_sz, [_i, _i, _i, _i, _i64]),
     "swa_attn_decode_ring": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i64, _f, _p, _sz, _p]),
     "swa_ring_slot_positions": (_i, [_i, _p, _i64, _p, _p]),
+    "swa_paged_append": (_i, [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _i, _i64, _i,
+                              _i, _i, _i, _p]),
+    "swa_chunk_paged_workspace_bytes": (_sz, [_i, _i64, _i, _i, _i]),
+    "swa_decode_paged_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "swa_attn_chunk_paged": (_i, [_p, _p, _p, _p, _p, _p, _i, _i64, _i, _i, _i, _i64, _i, _f, _i,
+                                  _p, _sz, _p]),
+    "swa_attn_decode_paged": (_i, [_p, _p, _p, _p, _p, _i, _i, _i, _i, _i64, _i, _f, _p, _sz, _p]),
     "swa_attn_decode_ring_static": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i64, _f, _p]),
     "swa_selftest_wait": (_i, [_i64, _i, _p, _p]),
     "swa_get_device_status": (_i, [_p]),

@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstdint>
 #include <atomic>
+#include <initializer_list>
 #include <cstring>
 #include <mutex>
 
@@ -20,6 +21,7 @@
 #include "swa_decode.cuh"
 #include "swa_fwd2.cuh"
 #include "swa_meta.cuh"
+#include "swa_paged.cuh"
 #include "swa_selftest.cuh"
 #include "swa_split.cuh"
 #include "swa_tile.cuh"
@@ -762,6 +764,187 @@ int swa_get_device_status(void *stream) {
   if (v & SWA_DEV_TIMEOUT) return SWA_ERR_TIMEOUT;
   if (v & SWA_DEV_BADARG) return SWA_ERR_DEVICE;
   return SWA_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The paged cache.
+// ---------------------------------------------------------------------------
+namespace {
+
+int paged_cache(const swa_paged_cache *c, int d, swa::PagedCache *out) {
+  if (!c || !c->k || !c->v || !c->table || !aligned16(c->k) || !aligned16(c->v) ||
+      (reinterpret_cast<uintptr_t>(c->table) & 3u))
+    return SWA_ERR_INVALID_ARG;
+  for (int64_t s : {c->page_stride, c->head_stride, c->slot_stride})
+    if (s < d || s % 8 != 0 || s >= (int64_t(1) << 39)) return SWA_ERR_INVALID_ARG;
+  if (c->page_size < 8 || c->page_size > 65536 || c->page_size % 8 != 0)
+    return SWA_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->n_pages >= 0x7FFFFFFF || c->max_pages < 1 ||
+      c->table_stride < c->max_pages || c->max_pages > (0x7FFFFFFF - 1024) / c->page_size)
+    return SWA_ERR_INVALID_ARG;
+  out->k = static_cast<__nv_bfloat16 *>(c->k);
+  out->v = static_cast<__nv_bfloat16 *>(c->v);
+  out->table = c->table;
+  out->page_stride = c->page_stride;
+  out->head_stride = c->head_stride;
+  out->slot_stride = c->slot_stride;
+  out->table_stride = c->table_stride;
+  out->n_pages = static_cast<int>(c->n_pages);
+  out->page_size = c->page_size;
+  out->max_pos = c->max_pages * c->page_size;
+  return SWA_OK;
+}
+
+int paged_checks(int n_seq, int64_t total, int H, int Hkv, int d, int64_t W, int n_sink,
+                 float scale) {
+  if (n_seq < 1 || H < 1 || Hkv < 1 || H % Hkv != 0) return SWA_ERR_INVALID_ARG;
+  if (total < 1 || total >= (int64_t(1) << 31) - 256) return SWA_ERR_INVALID_ARG;
+  if (W < 1 || !good_scale(scale) || n_sink < 0 || n_sink > kBK) return SWA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || n_seq >= (1 << 24)) return SWA_ERR_UNSUPPORTED;
+  return SWA_OK;
+}
+
+template <int D>
+int launch_paged_rows(const swa::PagedRowParams &p, cudaStream_t st) {
+  const int64_t blocks = (p.total * p.H + 3) / 4;
+  if (blocks > 0x7FFFFFFF) return SWA_ERR_UNSUPPORTED;
+  swa::paged_row_kernel<D><<<static_cast<unsigned>(blocks), 128, 0, st>>>(p);
+  return check_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+int swa_paged_append(const void *k_new, int64_t k_new_stride, const void *v_new,
+                     int64_t v_new_stride, const void *q, int64_t q_stride, void *q_out,
+                     int64_t q_out_stride, const swa_paged_cache *cache,
+                     const swa_rotation *rotation, const int64_t *cu_seqlens,
+                     const int64_t *q_start, int n_seq, int64_t total, int H, int Hkv, int d,
+                     int zero_rest, void *stream) {
+  if (!k_new || !v_new || !cu_seqlens || !q_start || !q != !q_out) return SWA_ERR_INVALID_ARG;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(q) || !aligned16(q_out))
+    return SWA_ERR_INVALID_ARG;
+  if (n_seq < 1 || Hkv < 1 || (q && H < 1)) return SWA_ERR_INVALID_ARG;
+  if (total < 1 || total >= (int64_t(1) << 31) - 256) return SWA_ERR_INVALID_ARG;
+  if ((d != 64 && d != 128) || n_seq >= (1 << 24) || Hkv > (1 << 20) || (q && H > (1 << 20)))
+    return SWA_ERR_UNSUPPORTED;
+  const int64_t kv_row = static_cast<int64_t>(Hkv) * d, q_row = static_cast<int64_t>(H) * d;
+  if (k_new_stride < kv_row || k_new_stride % 8 || v_new_stride < kv_row || v_new_stride % 8)
+    return SWA_ERR_INVALID_ARG;
+  if (q && (q_stride < q_row || q_stride % 8 || q_out_stride < q_row || q_out_stride % 8))
+    return SWA_ERR_INVALID_ARG;
+  if (q && q == q_out && q_stride != q_out_stride) return SWA_ERR_INVALID_ARG;
+  swa::AppendParams p = {};
+  int e = paged_cache(cache, d, &p.c);
+  if (e) return e;
+  if (rotation) {
+    if (!rotation->inv_freq || rotation->rot_dim < 16 || rotation->rot_dim > d ||
+        rotation->rot_dim % 16 != 0)
+      return SWA_ERR_INVALID_ARG;
+    if (rotation->positions &&
+        (rotation->n_axes < 1 || (rotation->n_axes > 1 && rotation->positions_stride < total)))
+      return SWA_ERR_INVALID_ARG;
+    if (rotation->pair_axis && !rotation->positions) return SWA_ERR_INVALID_ARG;
+    p.inv_freq = rotation->inv_freq;
+    p.positions = rotation->positions;
+    p.pair_axis = rotation->pair_axis;
+    p.pos_stride = rotation->positions_stride;
+    p.rot = rotation->rot_dim;
+    p.n_axes = rotation->n_axes;
+  }
+  p.k_new = static_cast<const __nv_bfloat16 *>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16 *>(v_new);
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+  p.k_stride = k_new_stride;
+  p.v_stride = v_new_stride;
+  p.q_stride = q_stride;
+  p.qo_stride = q_out_stride;
+  p.cu_seqlens = cu_seqlens;
+  p.q_start = q_start;
+  p.n_seq = n_seq;
+  p.total = total;
+  p.H = q ? H : 0;
+  p.Hkv = Hkv;
+  p.zero_rest = zero_rest;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  auto kern = rotation && rotation->interleaved
+                  ? (d == 128 ? swa::paged_append_kernel<128, true>
+                              : swa::paged_append_kernel<64, true>)
+                  : (d == 128 ? swa::paged_append_kernel<128, false>
+                              : swa::paged_append_kernel<64, false>);
+  kern<<<static_cast<unsigned>(total), swa::kAppendThreads, 0, st>>>(p);
+  return check_launch();
+}
+
+size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d) {
+  return paged_checks(n_seq, total, H, Hkv, d, 1, 0, 1.f) ? 0 : 256;
+}
+
+size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d) {
+  return paged_checks(B, B, H, Hkv, d, 1, 0, 1.f) ? 0 : 256;
+}
+
+int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int64_t *cu_seqlens,
+                         const int64_t *q_start, void *out, float *lse, int n_seq, int64_t total,
+                         int H, int Hkv, int d, int64_t W, int n_sink, float scale, int zero_rest,
+                         void *workspace, size_t workspace_bytes, void *stream) {
+  int e = paged_checks(n_seq, total, H, Hkv, d, W, n_sink, scale);
+  if (e) return e;
+  if (!q || !cu_seqlens || !q_start || !out || !aligned16(q) || !aligned16(out))
+    return SWA_ERR_INVALID_ARG;
+  if (H / Hkv > 128) return SWA_ERR_UNSUPPORTED;
+  swa::PagedRowParams p = {};
+  if ((e = paged_cache(cache, d, &p.c))) return e;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d))
+    return SWA_ERR_WORKSPACE;
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.cu_seqlens = cu_seqlens;
+  p.first = q_start;
+  p.n_seq = n_seq;
+  p.total = total;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.W = W;
+  p.n_sink = n_sink;
+  p.zero_rest = zero_rest;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_paged_rows<128>(p, st) : launch_paged_rows<64>(p, st);
+}
+
+int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int64_t *pos,
+                          void *out, float *lse, int B, int H, int Hkv, int d, int64_t W,
+                          int n_sink, float scale, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+  int e = paged_checks(B, B, H, Hkv, d, W, n_sink, scale);
+  if (e) return e;
+  if (!q || !pos || !out || !aligned16(q) || !aligned16(out)) return SWA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(B) * H > (1 << 24)) return SWA_ERR_UNSUPPORTED;
+  swa::PagedRowParams p = {};
+  if ((e = paged_cache(cache, d, &p.c))) return e;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < swa_decode_paged_workspace_bytes(B, H, Hkv, d))
+    return SWA_ERR_WORKSPACE;
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.out = static_cast<__nv_bfloat16 *>(out);
+  p.lse = lse;
+  p.first = pos;
+  p.n_seq = B;
+  p.total = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.W = W;
+  p.n_sink = n_sink;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return d == 128 ? launch_paged_rows<128>(p, st) : launch_paged_rows<64>(p, st);
 }
 
 }  // extern "C"

@@ -1,0 +1,292 @@
+// swa_paged.cuh -- the paged cache: its address arithmetic, and the append
+// kernel that rotates new keys (and queries) by their positions and writes
+// keys and values into the slots of their sequence's pages.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+
+#include "sm100.cuh"
+
+namespace swa {
+
+// Position p of sequence b: page table[b * table_stride + p / page_size], slot
+// p % page_size.  Strides in elements, shared by k and v.
+struct PagedCache {
+  __nv_bfloat16 *k = nullptr, *v = nullptr;
+  const int32_t *table = nullptr;
+  int64_t page_stride = 0, head_stride = 0, slot_stride = 0, table_stride = 0;
+  int n_pages = 0;
+  int page_size = 0;
+  int64_t max_pos = 0;  // positions a table row can map: max_pages * page_size
+};
+
+// ------------------------------------------------------------------ append
+//
+// One token per CTA.  Bound: bytes (every input row read once, every output
+// row written once); a step of few tokens is bound by the chain of dependent
+// loads offsets -> start -> table entry, so the token's rows are loaded into
+// registers before that chain starts and wait for nothing.
+//
+// The rotation of pair i turns (x, y) by a = position * inv_freq[i].  In 32
+// bits a would lose its fraction of a turn for far positions (position 10^5,
+// inv_freq 1: the product is rounded to 2^-8 of a radian), so the number of
+// turns a / 2 pi is formed in 64 bits, its integer part dropped there, and
+// only the remainder in [-1/2, 1/2] goes to the 32-bit sincospi.  One angle
+// per pair and token serves all H + Hkv heads through shared memory.
+constexpr int kAppendThreads = 128;
+constexpr int kAppendBatch = 4;  // 16-element items a thread keeps in flight
+
+struct AppendParams {
+  const __nv_bfloat16 *k_new, *v_new, *q;
+  __nv_bfloat16 *q_out;
+  int64_t k_stride, v_stride, q_stride, qo_stride;  // token strides, elements
+  PagedCache c;
+  const int64_t *cu_seqlens, *q_start;
+  int n_seq;
+  int64_t total;
+  int H, Hkv;  // H = 0: no queries
+  int zero_rest;
+  const float *inv_freq;
+  const int64_t *positions;  // nullptr: the position in the sequence
+  const int32_t *pair_axis;  // nullptr: axis 0
+  int64_t pos_stride;
+  int rot, n_axes;
+};
+
+// The number of i in [0, n] with cu[i] <= t, for non-decreasing cu (any value
+// in range otherwise): each round narrows the range by the CTA's thread count.
+__device__ __forceinline__ int64_t block_count_le(const int64_t *cu, int64_t n, int64_t t) {
+  int64_t lo = 0, len = n + 1;
+  while (len > 0) {
+    const int64_t step = (len + blockDim.x - 1) / blockDim.x;
+    const int64_t i = lo + (threadIdx.x + 1) * step - 1;
+    const int c = __syncthreads_count(i < lo + len && cu[i] <= t);
+    const int64_t end = lo + len;
+    lo += c * step;
+    len = step - 1 < end - lo ? step - 1 : end - lo;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void rotate_pair(float &x, float &y, float2 cs) {
+  const float a = x * cs.x - y * cs.y;
+  y = y * cs.x + x * cs.y;
+  x = a;
+}
+
+template <int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendParams p) {
+  constexpr int IPR = D / 16;  // items per row
+  __shared__ float2 s_cs[D / 2];
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x;
+  const int rows = p.H + 2 * p.Hkv, n_items = rows * IPR;
+  const int rot16 = p.rot / 16;
+  // Item i of a row is two 16-byte pieces: elements [8i, 8i+8) and their
+  // partners rot/2 further on (halves), or 16 consecutive ones (interleaved
+  // pairs, and whatever does not turn).
+  auto piece = [&](int item, int &row, int &i, int &e0, int &e1, bool &turns) {
+    row = item / IPR;
+    i = item % IPR;
+    turns = row < p.H + p.Hkv && i < rot16;
+    e0 = !INTERLEAVED && turns ? 8 * i : 16 * i;
+    e1 = !INTERLEAVED && turns ? p.rot / 2 + 8 * i : 16 * i + 8;
+  };
+  auto src_row = [&](int row) -> const __nv_bfloat16 * {
+    if (row < p.H) return p.q + t * p.q_stride + row * D;
+    if (row < p.H + p.Hkv) return p.k_new + t * p.k_stride + (row - p.H) * D;
+    return p.v_new + t * p.v_stride + (row - p.H - p.Hkv) * D;
+  };
+  uint4 a[kAppendBatch], b[kAppendBatch];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int u = 0; u < kAppendBatch; ++u) {
+      const int item = base + u * kAppendThreads + tid;
+      if (item >= n_items) break;
+      int row, i, e0, e1;
+      bool turns;
+      piece(item, row, i, e0, e1, turns);
+      const __nv_bfloat16 *src = src_row(row);
+      a[u] = *reinterpret_cast<const uint4 *>(src + e0);
+      b[u] = *reinterpret_cast<const uint4 *>(src + e1);
+    }
+  };
+  load(0);
+
+  if (blockIdx.x == 0) {  // offsets out of order or range: flagged once
+    for (int64_t i = tid; i < p.n_seq; i += kAppendThreads)
+      if (p.cu_seqlens[i] < 0 || p.cu_seqlens[i + 1] < p.cu_seqlens[i] ||
+          p.cu_seqlens[i + 1] > p.total)
+        atomicOr(&g_swa_status, SWA_DEV_BADARG);
+  }
+  const int64_t seq = block_count_le(p.cu_seqlens, p.n_seq, t) - 1;
+  int64_t pos = 0;
+  int page = -1;
+  if (seq >= 0 && seq < p.n_seq) {
+    const int64_t begin = p.cu_seqlens[seq], end = p.cu_seqlens[seq + 1];
+    const int64_t start = p.q_start[seq];
+    if (begin >= 0 && t >= begin && t < end && end <= p.total) {
+      pos = start + (t - begin);
+      if (start >= 0 && pos < p.c.max_pos)
+        page = p.c.table[seq * p.c.table_stride + pos / p.c.page_size];
+      if (page >= p.c.n_pages) page = -1;
+      if (page < 0 && tid == 0) atomicOr(&g_swa_status, SWA_DEV_BADARG);
+    }
+  }
+  if (page < 0) {  // no slot to write
+    if (p.zero_rest)
+      for (int i = tid; i < p.H * (D / 8); i += kAppendThreads)
+        *reinterpret_cast<uint4 *>(p.q_out + t * p.qo_stride + 8 * i) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const int64_t slot =
+      static_cast<int64_t>(page) * p.c.page_stride + (pos % p.c.page_size) * p.c.slot_stride;
+
+  if (tid < p.rot / 2) {
+    int64_t at = pos;
+    if (p.positions) {
+      int axis = p.pair_axis ? p.pair_axis[tid] : 0;
+      if (axis < 0 || axis >= p.n_axes) {
+        atomicOr(&g_swa_status, SWA_DEV_BADARG);
+        axis = 0;
+      }
+      at = p.positions[axis * p.pos_stride + t];
+    }
+    const double kInv2Pi = 0.15915494309189533577;
+    double turns = static_cast<double>(at) * (static_cast<double>(p.inv_freq[tid]) * kInv2Pi);
+    turns -= rint(turns);
+    float s, c;
+    sincospif(static_cast<float>(2.0 * turns), &s, &c);
+    s_cs[tid] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  for (int base = 0; base < n_items; base += kAppendBatch * kAppendThreads) {
+    if (base > 0) load(base);
+#pragma unroll
+    for (int u = 0; u < kAppendBatch; ++u) {
+      const int item = base + u * kAppendThreads + tid;
+      if (item >= n_items) break;
+      int row, i, e0, e1;
+      bool turns;
+      piece(item, row, i, e0, e1, turns);
+      if (turns) {
+        uint32_t wa[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+        uint32_t wb[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 x = make_float2(__uint_as_float(wa[j] << 16), __uint_as_float(wa[j] & 0xFFFF0000u));
+          float2 y = make_float2(__uint_as_float(wb[j] << 16), __uint_as_float(wb[j] & 0xFFFF0000u));
+          if (INTERLEAVED) {  // pairs inside each word
+            rotate_pair(x.x, x.y, s_cs[8 * i + j]);
+            rotate_pair(y.x, y.y, s_cs[8 * i + 4 + j]);
+          } else {
+            rotate_pair(x.x, y.x, s_cs[8 * i + 2 * j]);
+            rotate_pair(x.y, y.y, s_cs[8 * i + 2 * j + 1]);
+          }
+          wa[j] = pack_bf16(x.x, x.y);
+          wb[j] = pack_bf16(y.x, y.y);
+        }
+        a[u] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+        b[u] = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+      }
+      __nv_bfloat16 *dst;
+      if (row < p.H)
+        dst = p.q_out + t * p.qo_stride + row * D;
+      else if (row < p.H + p.Hkv)
+        dst = p.c.k + slot + (row - p.H) * p.c.head_stride;
+      else
+        dst = p.c.v + slot + (row - p.H - p.Hkv) * p.c.head_stride;
+      *reinterpret_cast<uint4 *>(dst + e0) = a[u];
+      *reinterpret_cast<uint4 *>(dst + e1) = b[u];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ attention, row by row
+//
+// One warp per (token, query head), keys one after another: the running
+// maximum, sum and output of a softmax in 32 bits.
+struct PagedRowParams {
+  const __nv_bfloat16 *q;
+  __nv_bfloat16 *out;
+  float *lse;
+  PagedCache c;
+  const int64_t *cu_seqlens;  // nullptr: decode, token b is sequence b at first[b]
+  const int64_t *first;
+  int n_seq;
+  int64_t total;
+  int H, Hkv, n_sink, zero_rest;
+  int64_t W;
+  float scale_log2;
+};
+
+template <int D>
+__global__ void __launch_bounds__(128) paged_row_kernel(const PagedRowParams p) {
+  constexpr int N = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (row >= p.total * p.H) return;
+  const int64_t t = row / p.H;
+  const int h = static_cast<int>(row % p.H), kvh = h / (p.H / p.Hkv);
+  const bool decode = p.cu_seqlens == nullptr;
+  int64_t pos = -1, seq = t;
+  if (decode) {
+    pos = p.first[t];
+    if (pos < -1 || pos >= p.c.max_pos) {
+      if (lane == 0) atomicOr(&g_swa_status, SWA_DEV_BADARG);
+      pos = -1;
+    }
+  } else {
+    if (row == 0)
+      for (int64_t i = lane; i < p.n_seq; i += 32)
+        if (p.cu_seqlens[i] < 0 || p.cu_seqlens[i + 1] < p.cu_seqlens[i] ||
+            p.cu_seqlens[i + 1] > p.total || p.first[i] < 0 ||
+            p.first[i] + p.cu_seqlens[i + 1] - p.cu_seqlens[i] > p.c.max_pos)
+          atomicOr(&g_swa_status, SWA_DEV_BADARG);
+    int n = 0;
+    for (int64_t i = lane; i <= p.n_seq; i += 32) n += p.cu_seqlens[i] <= t;
+    seq = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, n)) - 1;
+    if (seq < 0 || seq >= p.n_seq) {
+      if (!p.zero_rest) return;
+    } else {
+      const int64_t a = p.cu_seqlens[seq], e = p.cu_seqlens[seq + 1], s = p.first[seq];
+      if (a < 0 || t < a || t >= e || e > p.total || s < 0 || s + e - a > p.c.max_pos) return;
+      pos = s + t - a;
+    }
+  }
+  float q[N], o[N], m = -INFINITY, l = 0.f;
+  for (int i = 0; i < N; ++i) {
+    q[i] = __bfloat162float(p.q[row * D + lane * N + i]) * p.scale_log2;
+    o[i] = 0.f;
+  }
+  const int64_t low = pos - p.W + 1 > 0 ? pos - p.W + 1 : 0;
+  for (int64_t j = 0; j <= pos; ++j) {
+    if (j < low && j >= p.n_sink) j = low;
+    const int page = p.c.table[seq * p.c.table_stride + j / p.c.page_size];
+    const bool held = page >= 0 && page < p.c.n_pages;
+    if (!held && lane == 0) atomicOr(&g_swa_status, SWA_DEV_BADARG);
+    const int64_t at = static_cast<int64_t>(page) * p.c.page_stride + kvh * p.c.head_stride +
+                       (j % p.c.page_size) * p.c.slot_stride + lane * N;
+    float x = 0.f;
+    for (int i = 0; i < N; ++i) x += held ? q[i] * __bfloat162float(p.c.k[at + i]) : 0.f;
+    for (int o2 = 16; o2; o2 >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o2);
+    const float mn = fmaxf(m, x), al = ex2(m - mn), w = ex2(x - mn);
+    for (int i = 0; i < N; ++i)
+      o[i] = o[i] * al + (held ? w * __bfloat162float(p.c.v[at + i]) : 0.f);
+    l = l * al + w;
+    m = mn;
+  }
+  const bool none = pos < 0;
+  for (int i = 0; i < N; ++i)
+    p.out[row * D + lane * N + i] = __float2bfloat16_rn(none ? 0.f : o[i] / l);
+  if (p.lse && lane == 0) {
+    const float v = (m + __log2f(l)) * 0.6931471805599453f;
+    if (decode)
+      p.lse[row] = none ? -INFINITY : v;
+    else
+      p.lse[static_cast<int64_t>(h) * p.total + t] = none ? 0.f : v;
+  }
+}
+
+}  // namespace swa
