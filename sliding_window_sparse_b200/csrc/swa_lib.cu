@@ -22,6 +22,7 @@
 #include "swa_fwd2.cuh"
 #include "swa_meta.cuh"
 #include "swa_paged.cuh"
+#include "swa_paged_decode.cuh"
 #include "swa_selftest.cuh"
 #include "swa_split.cuh"
 #include "swa_tile.cuh"
@@ -806,6 +807,77 @@ int paged_checks(int n_seq, int64_t total, int H, int Hkv, int d, int64_t W, int
   return SWA_OK;
 }
 
+// 4-D bf16 map {d, slot, head, page} over a cache, boxes of 64 columns x box_rows
+// slots of one page and head; slots and pages out of bounds read as zero.
+int make_map_paged(CUtensorMap *m, const void *base, const swa::PagedCache &c, int d, int Hkv,
+                   int box_rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return SWA_ERR_CUDA;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.page_size),
+                        static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(c.n_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.slot_stride) * 2,
+                           static_cast<cuuint64_t>(c.head_stride) * 2,
+                           static_cast<cuuint64_t>(c.page_stride) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SWA_OK : SWA_ERR_CUDA;
+}
+
+// Slots per box: the largest power of two that divides the page, at most a
+// tile's 128, so that every box of an aligned tile lies in one page.
+int paged_box_rows(int page_size) {
+  const int g = page_size & -page_size;
+  return g < kBK ? g : kBK;
+}
+
+// Launches a merge kernel as a programmatic dependent of the kernel before it: its
+// CTAs start early and wait in griddepcontrol.wait for that kernel's results.
+template <typename Kernel, typename Params>
+int launch_dependent(Kernel kern, dim3 grid, int threads, const Params &p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return SWA_ERR_CUDA;
+  return check_launch();
+}
+
+// Runs that a paged attention call can split into: a bound that does not depend
+// on the device, so that a workspace has one size (148 SMs on a B200).
+constexpr int kPagedRuns = 148;
+
+struct DecodePagedWorkspace {
+  size_t run, ml, o, bytes;
+  explicit DecodePagedWorkspace(int d) {
+    const size_t slots = 2 * kPagedRuns * swa::kPDRows;
+    run = 0;
+    ml = align256(kPagedRuns * sizeof(int2));
+    o = ml + align256(slots * sizeof(float2));
+    bytes = o + align256(slots * d * sizeof(float));
+  }
+};
+
+template <int D>
+int launch_paged_decode(const CUtensorMap &tk, const CUtensorMap &tv,
+                        const swa::PagedDecodeParams &p, int grid, cudaStream_t st) {
+  using L = swa::PagedDecodeLayout<D>;
+  auto kern = swa::paged_decode_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) !=
+      cudaSuccess)
+    return SWA_ERR_CUDA;
+  kern<<<grid, swa::kPDThreads, L::ALLOC, st>>>(tk, tv, p);
+  if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
+  return launch_dependent(swa::paged_decode_merge_kernel<D>, dim3(grid), 128, p, st);
+}
+
 template <int D>
 int launch_paged_rows(const swa::PagedRowParams &p, cudaStream_t st) {
   const int64_t blocks = (p.total * p.H + 3) / 4;
@@ -885,7 +957,7 @@ size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv,
 }
 
 size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d) {
-  return paged_checks(B, B, H, Hkv, d, 1, 0, 1.f) ? 0 : 256;
+  return paged_checks(B, B, H, Hkv, d, 1, 0, 1.f) ? 0 : DecodePagedWorkspace(d).bytes;
 }
 
 int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int64_t *cu_seqlens,
@@ -927,7 +999,7 @@ int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int
   if (e) return e;
   if (!q || !pos || !out || !aligned16(q) || !aligned16(out)) return SWA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * H > (1 << 24)) return SWA_ERR_UNSUPPORTED;
-  swa::PagedRowParams p = {};
+  swa::PagedDecodeParams p = {};
   if ((e = paged_cache(cache, d, &p.c))) return e;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       workspace_bytes < swa_decode_paged_workspace_bytes(B, H, Hkv, d))
@@ -935,16 +1007,34 @@ int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int
   p.q = static_cast<const __nv_bfloat16 *>(q);
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
-  p.first = pos;
-  p.n_seq = B;
-  p.total = B;
+  p.pos = pos;
+  p.box_rows = paged_box_rows(p.c.page_size);
+  p.B = B;
   p.H = H;
   p.Hkv = Hkv;
-  p.W = W;
+  p.G = H / Hkv;
+  p.HB = (p.G + swa::kPDRows - 1) / swa::kPDRows;
   p.n_sink = n_sink;
+  p.W = W;
   p.scale_log2 = scale * 1.4426950408889634f;
+  const DecodePagedWorkspace ws(d);
+  char *w = static_cast<char *>(workspace);
+  p.ws_run = reinterpret_cast<int2 *>(w + ws.run);
+  p.ws_ml = reinterpret_cast<float2 *>(w + ws.ml);
+  p.ws_o = reinterpret_cast<float *>(w + ws.o);
+  CUtensorMap tk, tv;
+  if ((e = make_map_paged(&tk, p.c.k, p.c, d, Hkv, p.box_rows))) return e;
+  if ((e = make_map_paged(&tv, p.c.v, p.c, d, Hkv, p.box_rows))) return e;
+  // one CTA per SM, fewer where the longest sequences the call can have hold fewer tiles
+  const int64_t keys = W < p.c.max_pos ? W : p.c.max_pos;
+  const int64_t tiles = static_cast<int64_t>(B) * Hkv * p.HB * (keys / swa::kPDKeys + 3);
+  int sms = 0;
+  if (sm_count(&sms)) return SWA_ERR_CUDA;
+  int grid = sms < kPagedRuns ? sms : kPagedRuns;
+  if (tiles < grid) grid = static_cast<int>(tiles);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_paged_rows<128>(p, st) : launch_paged_rows<64>(p, st);
+  return d == 128 ? launch_paged_decode<128>(tk, tv, p, grid, st)
+                  : launch_paged_decode<64>(tk, tv, p, grid, st);
 }
 
 }  // extern "C"
