@@ -23,6 +23,7 @@
 #include "swa_meta.cuh"
 #include "swa_paged.cuh"
 #include "swa_paged_decode.cuh"
+#include "swa_paged_fwd.cuh"
 #include "swa_selftest.cuh"
 #include "swa_split.cuh"
 #include "swa_tile.cuh"
@@ -72,17 +73,17 @@ int make_map(CUtensorMap *m, const void *base, int d, int64_t rows, int64_t plan
 }
 
 // Token-major packed tensor [total, heads, d]: dims {d, heads, total}, box
-// {64, 1, box_rows} -- the same 128-byte-row swizzled tile in shared memory as
-// make_map's {64, box_rows, 1} box.
+// {64, box_heads, box_rows}: with one head the same 128-byte-row swizzled tile in
+// shared memory as make_map's {64, box_rows, 1} box, else a row per token and head.
 int make_map_tokens(CUtensorMap *m, const void *base, int d, int64_t heads, int64_t total,
-                    int box_rows) {
+                    int box_heads, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return SWA_ERR_CUDA;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(heads),
                         static_cast<cuuint64_t>(total)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
                            static_cast<cuuint64_t>(d) * 2 * static_cast<cuuint64_t>(heads)};
-  cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -120,6 +121,22 @@ int sm_count(int *sms) {
   return SWA_OK;
 }
 
+// The forward kernels' warpgroups re-split the registers they are launched with
+// (setmaxnreg); that split assumes exactly kFwd2LaunchRegs per thread.  The
+// count is read once per kernel variant; concurrent first calls may both read
+// it and store the same value.
+template <typename Kernel>
+int check_launch_regs(Kernel kern, std::atomic<int> &seen) {
+  int regs = seen.load(std::memory_order_relaxed);
+  if (regs < 0) {
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return SWA_ERR_CUDA;
+    regs = fa.numRegs;
+    seen.store(regs, std::memory_order_relaxed);
+  }
+  return regs == swa::kFwd2LaunchRegs ? SWA_OK : SWA_ERR_UNSUPPORTED;
+}
+
 // tks / tvs: the sink rows of the chunk-ring path with sinks (any map otherwise).
 // full_grid: one CTA per SM whatever the unit count (the split schedule's P).
 template <int D, int MODE, bool SINK = false>
@@ -132,19 +149,8 @@ int launch_fwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) !=
       cudaSuccess)
     return SWA_ERR_CUDA;
-  // The kernel's warpgroups re-split the registers it is launched with
-  // (setmaxnreg); that split assumes exactly kFwd2LaunchRegs per thread.
-  // The count is read once per kernel variant; concurrent first calls may
-  // both read it and store the same value.
   static std::atomic<int> launch_regs{-1};
-  int regs = launch_regs.load(std::memory_order_relaxed);
-  if (regs < 0) {
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return SWA_ERR_CUDA;
-    regs = fa.numRegs;
-    launch_regs.store(regs, std::memory_order_relaxed);
-  }
-  if (regs != swa::kFwd2LaunchRegs) return SWA_ERR_UNSUPPORTED;
+  if (int e = check_launch_regs(kern, launch_regs)) return e;
   const int64_t units = fwd_units(p);
   if (units > 0x7FFFFFFF) return SWA_ERR_UNSUPPORTED;
   p.n_units = static_cast<int>(units);
@@ -334,9 +340,9 @@ int swa_attn_varlen(const void *q, const void *k, const void *v, const int64_t *
   if (max_seqlen < 1 || max_seqlen >= (int64_t(1) << 29)) return SWA_ERR_INVALID_ARG;
   if (n_sink < 0 || n_sink > kBK) return SWA_ERR_INVALID_ARG;
   CUtensorMap tq, tk, tv;
-  if ((e = make_map_tokens(&tq, q, d, H, total, kBQ))) return e;
-  if ((e = make_map_tokens(&tk, k, d, Hkv, total, kBK))) return e;
-  if ((e = make_map_tokens(&tv, v, d, Hkv, total, kBK))) return e;
+  if ((e = make_map_tokens(&tq, q, d, H, total, 1, kBQ))) return e;
+  if ((e = make_map_tokens(&tk, k, d, Hkv, total, 1, kBK))) return e;
+  if ((e = make_map_tokens(&tv, v, d, Hkv, total, 1, kBK))) return e;
   swa::Fwd2Params p;
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
@@ -706,10 +712,10 @@ int swa_attn_varlen_bwd(const void *q, const void *k, const void *v, const int64
   const size_t need = swa_attn_varlen_bwd_workspace_bytes(H, total);
   if (!workspace || workspace_bytes < need || !aligned16(workspace)) return SWA_ERR_WORKSPACE;
   CUtensorMap tq, tk, tv, tdo;
-  if ((e = make_map_tokens(&tq, q, d, H, total, swa::kBwdT))) return e;
-  if ((e = make_map_tokens(&tk, k, d, Hkv, total, swa::kBwdT))) return e;
-  if ((e = make_map_tokens(&tv, v, d, Hkv, total, swa::kBwdT))) return e;
-  if ((e = make_map_tokens(&tdo, dout, d, H, total, swa::kBwdT))) return e;
+  if ((e = make_map_tokens(&tq, q, d, H, total, 1, swa::kBwdT))) return e;
+  if ((e = make_map_tokens(&tk, k, d, Hkv, total, 1, swa::kBwdT))) return e;
+  if ((e = make_map_tokens(&tv, v, d, Hkv, total, 1, swa::kBwdT))) return e;
+  if ((e = make_map_tokens(&tdo, dout, d, H, total, 1, swa::kBwdT))) return e;
   swa::BwdParams p;
   p.out = static_cast<const __nv_bfloat16 *>(out);
   p.dout = static_cast<const __nv_bfloat16 *>(dout);
@@ -807,20 +813,22 @@ int paged_checks(int n_seq, int64_t total, int H, int Hkv, int d, int64_t W, int
   return SWA_OK;
 }
 
-// 4-D bf16 map {d, slot, head, page} over a cache, boxes of 64 columns x box_rows
-// slots of one page and head; slots and pages out of bounds read as zero.
+// 5-D bf16 map {64 columns, slot, column panel, head, page} over a cache: a box is
+// box_rows slots of one page and head, in one panel of 64 columns or in all of them,
+// panel by panel; slots and pages out of bounds read as zero.
 int make_map_paged(CUtensorMap *m, const void *base, const swa::PagedCache &c, int d, int Hkv,
-                   int box_rows) {
+                   int box_rows, int box_panels) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return SWA_ERR_CUDA;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(c.page_size),
+  cuuint64_t dims[5] = {64, static_cast<cuuint64_t>(c.page_size), static_cast<cuuint64_t>(d / 64),
                         static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(c.n_pages)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.slot_stride) * 2,
+  cuuint64_t strides[4] = {static_cast<cuuint64_t>(c.slot_stride) * 2, 128,
                            static_cast<cuuint64_t>(c.head_stride) * 2,
                            static_cast<cuuint64_t>(c.page_stride) * 2};
-  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides,
+  cuuint32_t box[5] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_panels),
+                       1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides,
                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SWA_OK : SWA_ERR_CUDA;
@@ -878,12 +886,30 @@ int launch_paged_decode(const CUtensorMap &tk, const CUtensorMap &tv,
   return launch_dependent(swa::paged_decode_merge_kernel<D>, dim3(grid), 128, p, st);
 }
 
+struct ChunkPagedWorkspace {
+  size_t run, ml, o, bytes;
+  explicit ChunkPagedWorkspace(int d) {
+    const size_t rows = 2 * kPagedRuns * 2 * swa::kQT;
+    run = 0;
+    ml = align256(kPagedRuns * sizeof(int4));
+    o = ml + align256(rows * sizeof(float2));
+    bytes = o + align256(rows * d * sizeof(float));
+  }
+};
+
 template <int D>
-int launch_paged_rows(const swa::PagedRowParams &p, cudaStream_t st) {
-  const int64_t blocks = (p.total * p.H + 3) / 4;
-  if (blocks > 0x7FFFFFFF) return SWA_ERR_UNSUPPORTED;
-  swa::paged_row_kernel<D><<<static_cast<unsigned>(blocks), 128, 0, st>>>(p);
-  return check_launch();
+int launch_paged_fwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                     const swa::PagedFwdParams &p, int grid, cudaStream_t st) {
+  using L = swa::PagedFwdLayout<D>;
+  auto kern = swa::paged_fwd_kernel<D>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) !=
+      cudaSuccess)
+    return SWA_ERR_CUDA;
+  static std::atomic<int> launch_regs{-1};
+  if (int e = check_launch_regs(kern, launch_regs)) return e;
+  kern<<<grid, swa::kFwd2Threads, L::ALLOC, st>>>(tq, tk, tv, p);
+  if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
+  return launch_dependent(swa::paged_fwd_merge_kernel<D>, dim3(grid, 2, D / 16), swa::kQT, p, st);
 }
 
 }  // namespace
@@ -953,7 +979,7 @@ int swa_paged_append(const void *k_new, int64_t k_new_stride, const void *v_new,
 }
 
 size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d) {
-  return paged_checks(n_seq, total, H, Hkv, d, 1, 0, 1.f) ? 0 : 256;
+  return paged_checks(n_seq, total, H, Hkv, d, 1, 0, 1.f) ? 0 : ChunkPagedWorkspace(d).bytes;
 }
 
 size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d) {
@@ -969,26 +995,49 @@ int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int6
   if (!q || !cu_seqlens || !q_start || !out || !aligned16(q) || !aligned16(out))
     return SWA_ERR_INVALID_ARG;
   if (H / Hkv > 128) return SWA_ERR_UNSUPPORTED;
-  swa::PagedRowParams p = {};
+  swa::PagedFwdParams p = {};
   if ((e = paged_cache(cache, d, &p.c))) return e;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
       workspace_bytes < swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d))
     return SWA_ERR_WORKSPACE;
-  p.q = static_cast<const __nv_bfloat16 *>(q);
   p.out = static_cast<__nv_bfloat16 *>(out);
   p.lse = lse;
+  p.box_rows = paged_box_rows(p.c.page_size);
   p.cu_seqlens = cu_seqlens;
-  p.first = q_start;
+  p.q_start = q_start;
   p.n_seq = n_seq;
-  p.total = total;
+  p.total = static_cast<int>(total);
   p.H = H;
   p.Hkv = Hkv;
-  p.W = W;
+  p.G = H / Hkv;
+  p.tpt = kBQ / p.G;
+  p.g_inv = ((1 << 16) + p.G - 1) / p.G;
+  const int64_t slots = (total / (2 * p.tpt) + n_seq) * Hkv;
+  if (slots > (1 << 30)) return SWA_ERR_UNSUPPORTED;
+  p.n_slots = static_cast<int>(slots);
+  p.W = static_cast<int>(W < 0x7FFFFFFF - 1024 ? W : 0x7FFFFFFF - 1024);
   p.n_sink = n_sink;
   p.zero_rest = zero_rest;
   p.scale_log2 = scale * 1.4426950408889634f;
+  const ChunkPagedWorkspace ws(d);
+  char *w = static_cast<char *>(workspace);
+  p.ws_run = reinterpret_cast<int4 *>(w + ws.run);
+  p.ws_ml = reinterpret_cast<float2 *>(w + ws.ml);
+  p.ws_o = reinterpret_cast<float4 *>(w + ws.o);
+  CUtensorMap tq, tk, tv;
+  if ((e = make_map_tokens(&tq, q, d, H, total, p.G, p.tpt))) return e;
+  if ((e = make_map_paged(&tk, p.c.k, p.c, d, Hkv, p.box_rows, 1))) return e;
+  if ((e = make_map_paged(&tv, p.c.v, p.c, d, Hkv, p.box_rows, 1))) return e;
+  // one CTA per SM, fewer where the list cannot hold as many tiles
+  const int64_t keys = W < p.c.max_pos ? W : p.c.max_pos;
+  const int64_t tiles = slots * (keys / kBK + 4);
+  int sms = 0;
+  if (sm_count(&sms)) return SWA_ERR_CUDA;
+  int grid = sms < kPagedRuns ? sms : kPagedRuns;
+  if (tiles < grid) grid = static_cast<int>(tiles);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_paged_rows<128>(p, st) : launch_paged_rows<64>(p, st);
+  return d == 128 ? launch_paged_fwd<128>(tq, tk, tv, p, grid, st)
+                  : launch_paged_fwd<64>(tq, tk, tv, p, grid, st);
 }
 
 int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int64_t *pos,
@@ -1023,8 +1072,8 @@ int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int
   p.ws_ml = reinterpret_cast<float2 *>(w + ws.ml);
   p.ws_o = reinterpret_cast<float *>(w + ws.o);
   CUtensorMap tk, tv;
-  if ((e = make_map_paged(&tk, p.c.k, p.c, d, Hkv, p.box_rows))) return e;
-  if ((e = make_map_paged(&tv, p.c.v, p.c, d, Hkv, p.box_rows))) return e;
+  if ((e = make_map_paged(&tk, p.c.k, p.c, d, Hkv, p.box_rows, d / 64))) return e;
+  if ((e = make_map_paged(&tv, p.c.v, p.c, d, Hkv, p.box_rows, d / 64))) return e;
   // one CTA per SM, fewer where the longest sequences the call can have hold fewer tiles
   const int64_t keys = W < p.c.max_pos ? W : p.c.max_pos;
   const int64_t tiles = static_cast<int64_t>(B) * Hkv * p.HB * (keys / swa::kPDKeys + 3);

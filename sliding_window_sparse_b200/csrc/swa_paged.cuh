@@ -203,90 +203,4 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   }
 }
 
-// ------------------------------------------------------------------ attention, row by row
-//
-// One warp per (token, query head), keys one after another: the running
-// maximum, sum and output of a softmax in 32 bits.
-struct PagedRowParams {
-  const __nv_bfloat16 *q;
-  __nv_bfloat16 *out;
-  float *lse;
-  PagedCache c;
-  const int64_t *cu_seqlens;  // nullptr: decode, token b is sequence b at first[b]
-  const int64_t *first;
-  int n_seq;
-  int64_t total;
-  int H, Hkv, n_sink, zero_rest;
-  int64_t W;
-  float scale_log2;
-};
-
-template <int D>
-__global__ void __launch_bounds__(128) paged_row_kernel(const PagedRowParams p) {
-  constexpr int N = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= p.total * p.H) return;
-  const int64_t t = row / p.H;
-  const int h = static_cast<int>(row % p.H), kvh = h / (p.H / p.Hkv);
-  const bool decode = p.cu_seqlens == nullptr;
-  int64_t pos = -1, seq = t;
-  if (decode) {
-    pos = p.first[t];
-    if (pos < -1 || pos >= p.c.max_pos) {
-      if (lane == 0) atomicOr(&g_swa_status, SWA_DEV_BADARG);
-      pos = -1;
-    }
-  } else {
-    if (row == 0)
-      for (int64_t i = lane; i < p.n_seq; i += 32)
-        if (p.cu_seqlens[i] < 0 || p.cu_seqlens[i + 1] < p.cu_seqlens[i] ||
-            p.cu_seqlens[i + 1] > p.total || p.first[i] < 0 ||
-            p.first[i] + p.cu_seqlens[i + 1] - p.cu_seqlens[i] > p.c.max_pos)
-          atomicOr(&g_swa_status, SWA_DEV_BADARG);
-    int n = 0;
-    for (int64_t i = lane; i <= p.n_seq; i += 32) n += p.cu_seqlens[i] <= t;
-    seq = static_cast<int64_t>(__reduce_add_sync(0xffffffffu, n)) - 1;
-    if (seq < 0 || seq >= p.n_seq) {
-      if (!p.zero_rest) return;
-    } else {
-      const int64_t a = p.cu_seqlens[seq], e = p.cu_seqlens[seq + 1], s = p.first[seq];
-      if (a < 0 || t < a || t >= e || e > p.total || s < 0 || s + e - a > p.c.max_pos) return;
-      pos = s + t - a;
-    }
-  }
-  float q[N], o[N], m = -INFINITY, l = 0.f;
-  for (int i = 0; i < N; ++i) {
-    q[i] = __bfloat162float(p.q[row * D + lane * N + i]) * p.scale_log2;
-    o[i] = 0.f;
-  }
-  const int64_t low = pos - p.W + 1 > 0 ? pos - p.W + 1 : 0;
-  for (int64_t j = 0; j <= pos; ++j) {
-    if (j < low && j >= p.n_sink) j = low;
-    const int page = p.c.table[seq * p.c.table_stride + j / p.c.page_size];
-    const bool held = page >= 0 && page < p.c.n_pages;
-    if (!held && lane == 0) atomicOr(&g_swa_status, SWA_DEV_BADARG);
-    const int64_t at = static_cast<int64_t>(page) * p.c.page_stride + kvh * p.c.head_stride +
-                       (j % p.c.page_size) * p.c.slot_stride + lane * N;
-    float x = 0.f;
-    for (int i = 0; i < N; ++i) x += held ? q[i] * __bfloat162float(p.c.k[at + i]) : 0.f;
-    for (int o2 = 16; o2; o2 >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o2);
-    const float mn = fmaxf(m, x), al = ex2(m - mn), w = ex2(x - mn);
-    for (int i = 0; i < N; ++i)
-      o[i] = o[i] * al + (held ? w * __bfloat162float(p.c.v[at + i]) : 0.f);
-    l = l * al + w;
-    m = mn;
-  }
-  const bool none = pos < 0;
-  for (int i = 0; i < N; ++i)
-    p.out[row * D + lane * N + i] = __float2bfloat16_rn(none ? 0.f : o[i] / l);
-  if (p.lse && lane == 0) {
-    const float v = (m + __log2f(l)) * 0.6931471805599453f;
-    if (decode)
-      p.lse[row] = none ? -INFINITY : v;
-    else
-      p.lse[static_cast<int64_t>(h) * p.total + t] = none ? 0.f : v;
-  }
-}
-
 }  // namespace swa
