@@ -22,6 +22,9 @@
 //             looks the page of box i up a tile ahead and loads it.
 //   warp 1    one thread issues every tcgen05.mma: S_X = Q_X K^T and
 //             O_X += P_X V in the order PV_A(j), S_A(j+1), PV_B(j), S_B(j+1).
+//             (A thread for A and one for B would decouple the two, but then their
+//             MMAs and their softmaxes fall together instead of alternating: 667
+//             against 460 us for a prompt of 8192 tokens.)
 //   warp 2    scheduler: walks this CTA's run, 32 list entries at a time, and
 //             hands the units to the other roles through a ring.
 //   warp 3    idle.
@@ -78,8 +81,8 @@ struct PagedFwdLayout {
   static constexpr uint32_t Q_BYTES = kQT * D * 2, KV_BYTES = kKT * D * 2;
   static constexpr uint32_t OFF_QA = 0, OFF_QB = Q_BYTES, OFF_K = 2 * Q_BYTES;
   static constexpr uint32_t OFF_V = OFF_K + NK * KV_BYTES;
-  static constexpr uint32_t OFF_UNIT = OFF_V + NV * KV_BYTES;  // int4 [kUnitRing][2]
-  static constexpr uint32_t OFF_BAR = OFF_UNIT + kUnitRing * 32;
+  static constexpr uint32_t OFF_UNIT = OFF_V + NV * KV_BYTES;  // int4 [kUnitRing][4]
+  static constexpr uint32_t OFF_BAR = OFF_UNIT + kUnitRing * 64;
   // q_full, q_empty, k_full[NK], k_empty[NK], v_full[NV], v_empty[NV], s_full[2], p_full[2],
   // p2_full[2], o_full[2], mma_drain, u_full[kUnitRing], u_empty[kUnitRing]
   static constexpr int NBAR = 2 + 2 * NK + 2 * NV + 9 + 2 * kUnitRing;
@@ -88,44 +91,38 @@ struct PagedFwdLayout {
   static constexpr uint32_t TMEM_COLS = 512;
 };
 
-// One unit, as the scheduler hands it over.
+// One unit, as the scheduler hands it over: what its roles need, so that none of
+// them computes it on its way from one unit to the next.
 struct PagedUnit {
-  int b, kvh, tok, ntok;   // sequence, key/value head, first packed token, tokens
-  int qpos, t0, t1, n;     // position of the first token; the run's part [t0, t1) of n tiles
-};
+  int b, kvh, tok, ntok;  // sequence, key/value head, first packed token, tokens (0: the end)
+  int qpos, t0, t1, n;    // position of the first token; the run's part [t0, t1) of n tiles
+  // Key tiles in stream order: first + j, but tile 0 at j = 0 with `sink` (then first
+  // is the window's first tile less one).
+  int first, sink;
+  int low, last;          // lowest key of any window, last position
+  // Stream indices live for query tile A: t0 .. a_last (none if below t0); for B: b_first
+  // (a sink tile, or the first of the rest) and b_from .. b_last (none if b_last < t0).
+  int a_last, b_first, b_from, b_last;
 
-// The key tiles of a unit in stream order.  Tile A is live from the start to
-// its last row's tile, tile B from its first row's lowest key on (and in the
-// sink tile).
-struct PagedWalk {
-  int i, end, first, a_end, b_begin;
-  bool sink, has_b;
-  int low, last;      // lowest key of any window, last position
-  int qlo[2], qhi[2];
-  __device__ __forceinline__ void init(const PagedUnit &U, const PagedFwdParams &p) {
-    low = U.qpos - p.W + 1 > 0 ? U.qpos - p.W + 1 : 0;
-    last = U.qpos + U.ntok - 1;
+  __device__ __forceinline__ int tile(int j) const { return sink && j == 0 ? 0 : first + j; }
+  __device__ __forceinline__ bool live(int x, int j) const {
+    return x == 0 ? j <= a_last : j <= b_last && (j >= b_from || j == b_first);
+  }
+  // after b .. n are set
+  __device__ __forceinline__ void plan(const PagedFwdParams &p) {
+    low = qpos - p.W + 1 > 0 ? qpos - p.W + 1 : 0;
+    last = qpos + ntok - 1;
     first = low / kKT;
-    sink = p.n_sink > 0 && first > 0;
-    has_b = U.ntok > p.tpt;
-    qlo[0] = U.qpos;
-    qhi[0] = has_b ? U.qpos + p.tpt - 1 : last;
-    qlo[1] = U.qpos + p.tpt;
-    qhi[1] = last;
-    a_end = qhi[0] / kKT;
-    b_begin = (qlo[1] - p.W + 1 > 0 ? qlo[1] - p.W + 1 : 0) / kKT;
-    i = U.t0;
-    end = U.t1;
-  }
-  __device__ __forceinline__ int tile(int j) const {
-    return sink ? (j == 0 ? 0 : first + j - 1) : first + j;
-  }
-  __device__ __forceinline__ bool next(const PagedFwdParams &p, int &k, bool &ca, bool &cb) {
-    if (i >= end) return false;
-    k = tile(i++);
-    ca = k <= a_end;
-    cb = has_b && (k >= b_begin || (k == 0 && p.n_sink > 0));
-    return true;
+    sink = p.n_sink > 0 && first > 0 ? 1 : 0;
+    first -= sink;
+    const bool has_b = ntok > p.tpt;
+    const int a_hi = has_b ? qpos + p.tpt - 1 : last;  // A's last position
+    const int b_lo = qpos + p.tpt - p.W + 1;           // B's lowest key
+    a_last = min(a_hi / kKT - first, t1 - 1);
+    b_from = (b_lo > 0 ? b_lo : 0) / kKT - first;
+    // every row of B sees the sinks, in key tile 0
+    b_first = p.n_sink > 0 && tile(t0) == 0 ? t0 : max(b_from, t0);
+    b_last = !has_b || b_first >= t1 ? t0 - 1 : (b_from < t1 ? t1 - 1 : b_first);
   }
 };
 
@@ -135,31 +132,34 @@ struct PagedWalk {
 // is empty.  Returns the unit's key tiles (0: an empty entry).
 __device__ __forceinline__ int paged_unit(const PagedFwdParams &p, int u, PagedUnit &U) {
   if (u >= p.n_slots) return 0;
-  const int tu = 2 * p.tpt, q = u / p.Hkv;
-  auto base = [&](int b) -> int64_t {
+  const unsigned tu = 2 * p.tpt, q = static_cast<unsigned>(u) / p.Hkv;
+  auto offset = [&](int b) -> unsigned {  // in range, whatever the array holds
     const int64_t v = p.cu_seqlens[b];
-    return (v < 0 ? 0 : (v > p.total ? p.total : v)) / tu + b;
+    return v < 0 ? 0u : (v > p.total ? static_cast<unsigned>(p.total) : static_cast<unsigned>(v));
   };
   int lo = -1, hi = p.n_seq;  // the last sequence whose base is <= q
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (base(mid) <= q)
+    // cu / tu + mid <= q
+    if (static_cast<int64_t>(offset(mid)) <
+        (static_cast<int64_t>(q) - mid + 1) * static_cast<int64_t>(tu))
       lo = mid;
     else
       hi = mid;
   }
   if (lo < 0) return 0;
-  const int64_t b0 = base(lo), per = base(lo + 1) - b0;
-  if (per < 1) return 0;
-  const int64_t rem = u - b0 * p.Hkv, kvh = rem / per, tok = (rem - kvh * per) * tu;
   const int64_t a = p.cu_seqlens[lo], e = p.cu_seqlens[lo + 1], s = p.q_start[lo];
-  if (a < 0 || e > p.total || s < 0 || s + (e - a) > p.c.max_pos) return 0;
-  if (kvh >= p.Hkv || tok >= e - a) return 0;
+  if (a < 0 || e <= a || e > p.total || s < 0 || s + (e - a) > p.c.max_pos) return 0;
+  const unsigned b0 = static_cast<unsigned>(a) / tu + lo;
+  const unsigned per = static_cast<unsigned>(e) / tu + lo + 1 - b0;
+  const unsigned rem = u - b0 * p.Hkv, kvh = rem / per, tok = (rem - kvh * per) * tu;
+  const unsigned len = static_cast<unsigned>(e - a);
+  if (kvh >= static_cast<unsigned>(p.Hkv) || tok >= len) return 0;
   U.b = lo;
   U.kvh = static_cast<int>(kvh);
-  U.tok = static_cast<int>(a + tok);
-  U.ntok = static_cast<int>(e - a - tok < tu ? e - a - tok : tu);
-  U.qpos = static_cast<int>(s + tok);
+  U.tok = static_cast<int>(a) + static_cast<int>(tok);
+  U.ntok = static_cast<int>(len - tok < tu ? len - tok : tu);
+  U.qpos = static_cast<int>(s) + static_cast<int>(tok);
   const int low = U.qpos - p.W + 1 > 0 ? U.qpos - p.W + 1 : 0, first = low / kKT;
   U.n = (U.qpos + U.ntok - 1) / kKT - first + 1 + (p.n_sink > 0 && first > 0 ? 1 : 0);
   return U.n;
@@ -176,7 +176,6 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t *gbase = smem_raw + (base - raw);
-  const uint32_t sQ[2] = {base + L::OFF_QA, base + L::OFF_QB};
   const uint32_t sK = base + L::OFF_K, sV = base + L::OFF_V, bar = base + L::OFF_BAR;
   const uint32_t BAR_QF = bar, BAR_QE = bar + 8;
   const uint32_t BAR_KF = bar + 16;             // + 8 * K stage
@@ -235,9 +234,10 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   // CTAs or T if that is less.  List position s is column s / rows, row s % rows of
   // the matrix of units.  Every CTA sums the costs, a contiguous piece per thread.
   const int n_cols = gridDim.x, n_rows = (p.n_slots + n_cols - 1) / n_cols;
-  const int64_t n_list = static_cast<int64_t>(n_rows) * n_cols;
-  auto unit_at = [&](int64_t s, PagedUnit &U) -> int {
-    return paged_unit(p, static_cast<int>((s % n_rows) * n_cols + s / n_rows), U);
+  const int n_list = n_rows * n_cols;
+  auto unit_at = [&](int s, PagedUnit &U) -> int {
+    const int col = s / n_rows;
+    return paged_unit(p, (s - col * n_rows) * n_cols + col, U);
   };
   int64_t T = 0, lo, hi;
   int P;
@@ -249,10 +249,11 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
           atomicOr(&g_swa_status, SWA_DEV_BADARG);
       }
     int64_t *s_warp = reinterpret_cast<int64_t *>(gbase);
-    const int64_t per = (n_list + kFwd2Threads - 1) / kFwd2Threads;
-    const int64_t s_lo = min(threadIdx.x * per, n_list), s_hi = min(s_lo + per, n_list);
+    const int per = (n_list + kFwd2Threads - 1) / kFwd2Threads;
+    const int s_lo = min(static_cast<int>(threadIdx.x) * per, n_list);
+    const int s_hi = min(s_lo + per, n_list);
     int64_t sum = 0;
-    for (int64_t s = s_lo; s < s_hi; ++s) {
+    for (int s = s_lo; s < s_hi; ++s) {
       PagedUnit U;
       const int n = unit_at(s, U);
       sum += n ? n + kUnitCost : 0;
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
     lo = c < P ? T * c / P : 0;
     hi = c < P ? T * (c + 1) / P : 0;
     if (hi > lo && lo >= at && lo < at + sum) {
-      for (int64_t s = s_lo; s < s_hi; ++s) {
+      for (int s = s_lo; s < s_hi; ++s) {
         PagedUnit U;
         const int n = unit_at(s, U);
         if (n && lo < at + n + kUnitCost) {
@@ -295,15 +296,24 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   // Next unit from the scheduler; false at the end of the run.  Each warp (or
   // thread) that takes it frees it with unit_done.
   auto unit_load = [&](int it, PagedUnit &U) -> bool {
-    const int4 a = s_unit[2 * (it % kUnitRing)], e = s_unit[2 * (it % kUnitRing) + 1];
+    const int4 *e = s_unit + 4 * (it % kUnitRing);
+    const int4 a = e[0], c = e[1], d = e[2], f = e[3];
     U.b = a.x;
     U.kvh = a.y;
     U.tok = a.z;
     U.ntok = a.w;
-    U.qpos = e.x;
-    U.t0 = e.y;
-    U.t1 = e.z;
-    U.n = e.w;
+    U.qpos = c.x;
+    U.t0 = c.y;
+    U.t1 = c.z;
+    U.n = c.w;
+    U.first = d.x;
+    U.sink = d.y;
+    U.low = d.z;
+    U.last = d.w;
+    U.a_last = f.x;
+    U.b_first = f.y;
+    U.b_from = f.z;
+    U.b_last = f.w;
     return U.ntok > 0;
   };
   auto unit_bar = [&](int it) -> uint32_t { return BAR_UF + 8 * (it % kUnitRing); };
@@ -325,15 +335,13 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         __syncwarp();
         if (lane == 0) unit_done(it);
         if (!any) break;
-        PagedWalk w;
-        w.init(U, p);
         const int32_t *row = p.c.table + U.b * p.c.table_stride;
         // this lane's box of tile j: its page and first slot (-1: no visible key lies there)
         auto look_up = [&](int j, int &slot) -> int {
           slot = -1;
           if (j >= U.t1 || lane >= boxes) return 0;
-          const int at = w.tile(j) * kKT + lane * p.box_rows;
-          if (at > w.last || (at + p.box_rows <= w.low && at >= p.n_sink)) return 0;
+          const int at = U.tile(j) * kKT + lane * p.box_rows;
+          if (at > U.last || (at + p.box_rows <= U.low && at >= p.n_sink)) return 0;
           const int pg = at / p.c.page_size;
           slot = at - pg * p.c.page_size;
           return row[pg];
@@ -342,14 +350,15 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         if (lane == 0) {
           ok = q_iter == 0 || mbar_wait(BAR_QE, (q_iter - 1) & 1, abort_flag);
           if (ok) {
-            mbar_expect_tx(BAR_QF, (w.has_b ? 2 : 1) * q_bytes);
+            const bool has_b = U.ntok > p.tpt;
+            mbar_expect_tx(BAR_QF, (has_b ? 2 : 1) * q_bytes);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              if (x == 1 && !w.has_b) break;
+              if (x == 1 && !has_b) break;
 #pragma unroll
               for (int pn = 0; pn < L::PANELS; ++pn)
-                tma_load_3d(sQ[x] + pn * (kQT * 128), &tm_q, BAR_QF, pn * 64, U.kvh * p.G,
-                            U.tok + x * p.tpt);
+                tma_load_3d(base + L::OFF_QA + x * L::Q_BYTES + pn * (kQT * 128), &tm_q, BAR_QF,
+                            pn * 64, U.kvh * p.G, U.tok + x * p.tpt);
             }
           }
         }
@@ -412,11 +421,12 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       }
     } else if (warp == 1) {
       // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
+      if (elect_one()) {
         constexpr uint32_t idS = idesc_bf16_f32(kQT, kKT, false);
         constexpr uint32_t idO = idesc_bf16_f32(kQT, D, true);
         constexpr uint32_t kDescHi = sdesc_sw128_hi(1024);
-        const uint32_t q_lo[2] = {sdesc_sw128_lo(sQ[0], 16), sdesc_sw128_lo(sQ[1], 16)};
+        const uint32_t q_lo[2] = {sdesc_sw128_lo(base + L::OFF_QA, 16),
+                                  sdesc_sw128_lo(base + L::OFF_QB, 16)};
         const uint32_t k_lo = sdesc_sw128_lo(sK, 16), v_lo = sdesc_sw128_lo(sV, kKT * 128);
         int kv = 0, q_iter = 0;
         uint32_t p_cnt[2] = {0u, 0u};
@@ -463,13 +473,11 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
           const bool any = unit_load(it, U);
           unit_done(it);
           if (!any) break;
-          PagedWalk w;
-          w.init(U, p);
           if (!mbar_wait(BAR_QF, q_iter & 1, abort_flag)) break;
           tc_fence_after();
-          int k;
-          bool ca, cb, na = false, nb = false;
-          bool have = w.next(p, k, ca, cb), has_next = w.next(p, k, na, nb);
+          int j = U.t0;
+          bool ca = U.live(0, j), cb = U.live(1, j), have = true, has_next = ++j < U.t1;
+          bool na = has_next && U.live(0, j), nb = has_next && U.live(1, j);
           if (!k_wait(kv)) break;
           if (ca) issue_s(0, kv % NK);
           if (cb) issue_s(1, kv % NK);
@@ -483,8 +491,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
           }
           tc_commit(BAR_KE + 8 * (kv % NK));
           bool first[2] = {true, true}, o_done[2] = {false, false};
-          const bool b_contig = !w.sink;  // else B may pause between the sinks and its window
-          bool stop = false;              // a wait gave up: issue nothing more
+          bool stop = false;  // a wait gave up: issue nothing more
           while (have) {
             if (!has_next) tc_commit(BAR_QE);  // every S of this unit is issued
             const int sv = kv % NV, skn = (kv + 1) % NK;
@@ -498,7 +505,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
                 break;
               }
               first[0] = false;
-              if (!(has_next && na)) {  // A's live tiles are contiguous
+              if (j - 1 == U.a_last) {
                 tc_commit(BAR_O);
                 o_done[0] = true;
               }
@@ -516,7 +523,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
                 break;
               }
               first[1] = false;
-              if (b_contig && !(has_next && nb)) {
+              if (j - 1 == U.b_last) {
                 tc_commit(BAR_O + 8);
                 o_done[1] = true;
               }
@@ -531,7 +538,9 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             ca = na;
             cb = nb;
             have = has_next;
-            if (have) has_next = w.next(p, k, na, nb);
+            has_next = ++j < U.t1;
+            na = has_next && U.live(0, j);
+            nb = has_next && U.live(1, j);
           }
           if (stop) break;
           // o_full completes once per unit in which the tile had work; its next
@@ -555,13 +564,16 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         if (it >= kUnitRing &&
             !mbar_wait(BAR_UE + 8 * r, ((it / kUnitRing) - 1) & 1, abort_flag))
           return false;
-        s_unit[2 * r] = make_int4(U.b, U.kvh, U.tok, U.ntok);
-        s_unit[2 * r + 1] = make_int4(U.qpos, U.t0, U.t1, U.n);
+        s_unit[4 * r] = make_int4(U.b, U.kvh, U.tok, U.ntok);
+        s_unit[4 * r + 1] = make_int4(U.qpos, U.t0, U.t1, U.n);
+        s_unit[4 * r + 2] = make_int4(U.first, U.sink, U.low, U.last);
+        s_unit[4 * r + 3] = make_int4(U.a_last, U.b_first, U.b_from, U.b_last);
         mbar_arrive(BAR_UF + 8 * r);
         return true;
       };
       if (hi > lo) {
-        int64_t s = s_run[0], at = s_run[1];
+        int s = static_cast<int>(s_run[0]);
+        int64_t at = s_run[1];
         while (ok && at < hi && s < n_list) {
           PagedUnit U;
           const int n = s + lane < n_list ? unit_at(s + lane, U) : 0;
@@ -579,6 +591,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             // run j begins inside iff floor(T j / P) < a + n iff j < (a + n) P / T
             p.ws_run[blockIdx.x] = make_int4(U.tok, U.kvh, U.ntok,
                                              static_cast<int>(((a + n) * P + T - 1) / T));
+          if (n) U.plan(p);
           uint32_t todo = __ballot_sync(0xffffffffu, n && U.t0 < U.t1);
           for (; todo && ok; todo &= todo - 1, ++it) {
             const int i = __ffs(todo) - 1;
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
           s += 32;
         }
       }
-      PagedUnit none = {0, 0, 0, 0, 0, 0, 0, 0};
+      PagedUnit none = {};
       if (ok && lane == 0) publish(none);
     }
   } else {
@@ -612,16 +625,13 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       __syncwarp();
       if (lane == 0) unit_done(it);
       if (!any) break;
-      PagedWalk w;
-      w.init(U, p);
-      const int qlo = x ? w.qlo[1] : w.qlo[0], qhi = x ? w.qhi[1] : w.qhi[0];
+      const int qlo = U.qpos + x * p.tpt, qhi = min(qlo + p.tpt - 1, U.last);
       const int qrow = qlo + row_t;
       float m_run = -INFINITY, l_run = 0.f;
       int nt = 0;
-      int k;
-      bool ca, cb;
-      while (w.next(p, k, ca, cb)) {
-        if (!(x == 0 ? ca : cb)) continue;
+      for (int j = U.t0; j < U.t1; ++j) {
+        if (!U.live(x, j)) continue;
+        const int k = U.tile(j);
         if (!mbar_wait_warp(BAR_S + 8 * x, s_cnt & 1, abort_flag)) {
           stop = true;
           break;
@@ -642,16 +652,16 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             mw[i] = range_bits(lo_c - 32 * i, hi_c - 32 * i) | range_bits(-32 * i, sink_c - 32 * i);
 #pragma unroll
           for (int c = 0; c < kKT; ++c) s[c] = ((mw[c >> 5] >> (c & 31)) & 1u) ? s[c] : -INFINITY;
-          if (k0 + kKT - 1 > w.last || k0 < w.low) {
+          if (k0 + kKT - 1 > U.last || k0 < U.low) {
             // value rows that no query of the unit sees (one row per thread, its pieces
             // in an order that spreads a warp over the banks)
-            const int i = kv0 + w.i - 1 - U.t0;
+            const int i = kv0 + j - U.t0;
             if (!mbar_wait_warp(BAR_VF + 8 * (i % NV), (i / NV) & 1, abort_flag)) {
               stop = true;
               break;
             }
             const int key = k0 + row;
-            if (key > w.last || (key < w.low && key >= p.n_sink)) {
+            if (key > U.last || (key < U.low && key >= p.n_sink)) {
 #pragma unroll
               for (int c = 0; c < D / 8; ++c)
                 st_shared_v4(sV + (i % NV) * L::KV_BYTES + (c >> 3) * (kKT * 128) + row * 128 +
