@@ -460,51 +460,62 @@ def swa_ring_slot_positions(n_written, W: int, out=None):
     return out
 
 
-def _one_device(first, **others):
-    """All tensors on one CUDA device; a context in which it is the current one."""
-    dev = first.device
-    for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    return (contextlib.nullcontext() if torch.cuda.current_device() == dev.index
-            else torch.cuda.device(dev))
+# The paged calls serve single tokens, where the host's time counts: their checks ask each tensor
+# once, and the stream comes without a Python object around it (2 us).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _one_device(index, *named):
+    """All tensors on CUDA device `index`; a context in which it is the current one."""
+    for name, t in named:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    return (_CURRENT if torch.cuda.current_device() == index else torch.cuda.device(index))
+
+
+_CURRENT = contextlib.nullcontext()
 
 
 def _need_rows(t, name, shape):
     """bf16 [tokens, heads, d] whose token rows may lie apart (a slice of a fused projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape):
+    if not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != shape:
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor of shape {list(shape)}, got "
                          f"{t.dtype} {list(t.shape)} on {t.device}")
-    heads, d = shape[1:]
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
+    total, heads, d = shape
+    apart, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != d):
         raise ValueError(f"{name} must hold each token's [heads, d] contiguously")
-    return t.stride(0) if shape[0] > 1 else heads * d
+    return apart if total > 1 else heads * d
 
 
 def _need_int(t, name, dtype, shape):
     _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
-def _paged_cache(k_cache, v_cache, block_table, n_seq, Hkv, d):
+def _paged_cache(k_cache, v_cache, block_table, n_seq):
+    """The cache's structure for the library, its heads and head dim."""
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{n} must be a torch.Tensor")
         if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4:
             raise ValueError(f"{n} must be a bfloat16 CUDA tensor [n_pages, Hkv, page_size, d]")
-        if t.stride(3) != 1:
-            raise ValueError(f"{n} must be contiguous in its last dimension")
-    n_pages, heads, page_size, dk = k_cache.shape
-    # the stride of a dimension of one entry says nothing: any valid one will do
-    strides = [k_cache.stride(i) if k_cache.shape[i] > 1 else dk for i in range(3)]
-    if v_cache.shape != k_cache.shape or \
-            [v_cache.stride(i) if v_cache.shape[i] > 1 else dk for i in range(3)] != strides:
+    shape, strides = k_cache.shape, k_cache.stride()
+    n_pages, heads, page_size, d = shape
+    same = v_cache.shape == shape and v_cache.stride() == strides
+    if 1 in shape[:3]:
+        # the stride of a dimension of one entry says nothing: any valid one will do
+        other = v_cache.stride()
+        same = v_cache.shape == shape and all(n == 1 or a == b for n, a, b in
+                                              zip(shape, strides, other))
+        strides = [d if n == 1 else s for n, s in zip(shape[:3], strides)] + [strides[3]]
+    if not same:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    if heads != Hkv or dk != d:
-        raise ValueError(f"the cache has {heads} heads of {dk}, expected {Hkv} of {d}")
+    if strides[3] != 1:
+        raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
     if not isinstance(block_table, torch.Tensor):
         raise TypeError("block_table must be a torch.Tensor")
     if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
@@ -513,9 +524,9 @@ def _paged_cache(k_cache, v_cache, block_table, n_seq, Hkv, d):
         raise ValueError(f"block_table must be an int32 CUDA tensor [{n_seq}, max_pages], "
                          "contiguous along a row")
     max_pages = block_table.shape[1]
-    return PagedCache(_ptr(k_cache), _ptr(v_cache), _ptr(block_table), strides[0], strides[1],
-                      strides[2], n_pages, max_pages,
-                      block_table.stride(0) if n_seq > 1 else max_pages, page_size)
+    return (PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), strides[0],
+                       strides[1], strides[2], n_pages, max_pages,
+                       block_table.stride(0) if n_seq > 1 else max_pages, page_size), heads, d)
 
 
 def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_start, q=None,
@@ -534,23 +545,27 @@ def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_
     """
     if not isinstance(k_new, torch.Tensor) or k_new.dim() != 3:
         raise ValueError("k_new must be [total, Hkv, d]")
-    total, Hkv, d = k_new.shape
-    ks = _need_rows(k_new, "k_new", (total, Hkv, d))
-    vs = _need_rows(v_new, "v_new", (total, Hkv, d))
+    total, Hkv, d = shape = k_new.shape
+    ks = _need_rows(k_new, "k_new", shape)
+    vs = _need_rows(v_new, "v_new", shape)
     _need(cu_seqlens, "cu_seqlens", torch.int64, 1)
     n_seq = cu_seqlens.shape[0] - 1
     _need_int(q_start, "q_start", torch.int64, (n_seq,))
-    cache = _paged_cache(k_cache, v_cache, block_table, n_seq, Hkv, d)
+    cache, heads, dk = _paged_cache(k_cache, v_cache, block_table, n_seq)
+    if heads != Hkv or dk != d:
+        raise ValueError(f"the cache has {heads} heads of {dk}, expected {Hkv} of {d}")
     H, qs, qos, zero_rest = 0, 0, 0, False
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q must be [total, H, d]")
         H = q.shape[1]
         qs = _need_rows(q, "q", (total, H, d))
-        zero_rest = q_out is None
-        if zero_rest:
-            q_out = torch.empty((total, H, d), dtype=q.dtype, device=q.device)
-        qos = _need_rows(q_out, "q_out", (total, H, d))
+        if q_out is None:
+            zero_rest = True
+            q_out = q.new_empty((total, H, d))
+            qos = H * d
+        else:
+            qos = _need_rows(q_out, "q_out", (total, H, d))
     elif q_out is not None:
         raise ValueError("q_out without q")
     rotation = None
@@ -571,15 +586,17 @@ def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_
                             1 if interleaved else 0, n_axes)
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need inv_freq")
-    with _one_device(k_new, v_new=v_new, k_cache=k_cache, v_cache=v_cache,
-                     block_table=block_table, cu_seqlens=cu_seqlens, q_start=q_start, q=q,
-                     q_out=q_out, inv_freq=inv_freq, positions=positions, pair_axis=pair_axis):
+    index = k_new.get_device()
+    with _one_device(index, ("v_new", v_new), ("k_cache", k_cache), ("v_cache", v_cache),
+                     ("block_table", block_table), ("cu_seqlens", cu_seqlens),
+                     ("q_start", q_start), ("q", q), ("q_out", q_out), ("inv_freq", inv_freq),
+                     ("positions", positions), ("pair_axis", pair_axis)):
         check("swa_paged_append",
-              lib().swa_paged_append(_ptr(k_new), ks, _ptr(v_new), vs, _ptr(q), qs, _ptr(q_out),
-                                     qos, ctypes.byref(cache),
+              lib().swa_paged_append(k_new.data_ptr(), ks, v_new.data_ptr(), vs, _ptr(q), qs,
+                                     _ptr(q_out), qos, ctypes.byref(cache),
                                      ctypes.byref(rotation) if rotation else None,
-                                     _ptr(cu_seqlens), _ptr(q_start), n_seq, total, H, Hkv, d,
-                                     1 if zero_rest else 0, _stream(k_new.device)))
+                                     cu_seqlens.data_ptr(), q_start.data_ptr(), n_seq, total, H,
+                                     Hkv, d, 1 if zero_rest else 0, _raw_stream(index)))
     return q_out
 
 
@@ -602,38 +619,41 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
     total, H, d = q.shape
     n_seq = cu_seqlens.shape[0] - 1
     _need_int(q_start, "q_start", torch.int64, (n_seq,))
-    Hkv = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
-    cache = _paged_cache(k_cache, v_cache, block_table, n_seq, Hkv, d)
+    cache, Hkv, dk = _paged_cache(k_cache, v_cache, block_table, n_seq)
+    if dk != d:
+        raise ValueError(f"the cache has heads of {dk}, q of {d}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     new_out, new_lse = out is None, return_lse and lse is None
-    if out is not None:
+    if not new_out:
         _need(out, "out", dims=3)
         if out.shape != q.shape:
             raise ValueError("out must match q")
     if lse is not None:
         _need_int(lse, "lse", torch.float32, (H, total))
-    with _one_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
-                     cu_seqlens=cu_seqlens, q_start=q_start, out=out, lse=lse,
-                     workspace=workspace):
+    index = q.get_device()
+    with _one_device(index, ("k_cache", k_cache), ("v_cache", v_cache),
+                     ("block_table", block_table), ("cu_seqlens", cu_seqlens),
+                     ("q_start", q_start), ("out", out), ("lse", lse), ("workspace", workspace)):
         # what is allocated here is zeroed by the call outside the sequences, unless the other
         # of the two is the caller's: then its rows stay, and ours are zeroed first
         zero_rest = new_out and (new_lse or lse is None)
-        make = torch.empty if zero_rest else torch.zeros
         if new_out:
-            out = make(q.shape, dtype=q.dtype, device=q.device)
+            out = torch.empty_like(q) if zero_rest else torch.zeros_like(q)
         if new_lse:
-            lse = make((H, total), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((H, total), dtype=torch.float32)
+            if not zero_rest:
+                lse.zero_()
         if workspace is None:
             need = swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
         check("swa_attn_chunk_paged",
-              lib().swa_attn_chunk_paged(_ptr(q), ctypes.byref(cache), _ptr(cu_seqlens),
-                                         _ptr(q_start), _ptr(out), _ptr(lse), n_seq, total, H, Hkv,
-                                         d, W, n_sink, scale, 1 if zero_rest else 0,
-                                         _ptr(workspace),
+              lib().swa_attn_chunk_paged(q.data_ptr(), ctypes.byref(cache), cu_seqlens.data_ptr(),
+                                         q_start.data_ptr(), out.data_ptr(), _ptr(lse), n_seq,
+                                         total, H, Hkv, d, W, n_sink, scale,
+                                         1 if zero_rest else 0, workspace.data_ptr(),
                                          workspace.numel() * workspace.element_size(),
-                                         _stream(q.device)))
+                                         _raw_stream(index)))
     return (out, lse) if return_lse else out
 
 
@@ -652,8 +672,9 @@ def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
     _need(q, "q", dims=3)
     B, H, d = q.shape
     _need_int(pos, "pos", torch.int64, (B,))
-    Hkv = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
-    cache = _paged_cache(k_cache, v_cache, block_table, B, Hkv, d)
+    cache, Hkv, dk = _paged_cache(k_cache, v_cache, block_table, B)
+    if dk != d:
+        raise ValueError(f"the cache has heads of {dk}, q of {d}")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if out is not None:
@@ -662,21 +683,23 @@ def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
             raise ValueError("out must match q")
     if lse is not None:
         _need_int(lse, "lse", torch.float32, (B, H))
-    with _one_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, pos=pos,
-                     out=out, lse=lse, workspace=workspace):
+    index = q.get_device()
+    with _one_device(index, ("k_cache", k_cache), ("v_cache", v_cache),
+                     ("block_table", block_table), ("pos", pos), ("out", out), ("lse", lse),
+                     ("workspace", workspace)):
         if out is None:
             out = torch.empty_like(q)
         if return_lse and lse is None:
-            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, H), dtype=torch.float32)
         if workspace is None:
             need = swa_decode_paged_workspace_bytes(B, H, Hkv, d)
-            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
         check("swa_attn_decode_paged",
-              lib().swa_attn_decode_paged(_ptr(q), ctypes.byref(cache), _ptr(pos), _ptr(out),
-                                          _ptr(lse), B, H, Hkv, d, W, n_sink, scale,
-                                          _ptr(workspace),
+              lib().swa_attn_decode_paged(q.data_ptr(), ctypes.byref(cache), pos.data_ptr(),
+                                          out.data_ptr(), _ptr(lse), B, H, Hkv, d, W, n_sink,
+                                          scale, workspace.data_ptr(),
                                           workspace.numel() * workspace.element_size(),
-                                          _stream(q.device)))
+                                          _raw_stream(index)))
     return (out, lse) if return_lse else out
 
 

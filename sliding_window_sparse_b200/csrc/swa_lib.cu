@@ -858,6 +858,31 @@ int launch_dependent(Kernel kern, dim3 grid, int threads, const Params &p, cudaS
   return check_launch();
 }
 
+// What a launch has to know of the current device, and a kernel's permission to use
+// `smem` bytes there: asked once per device (concurrent first calls may both ask;
+// they store the same value).  `done` is the kernel's own, bit i for device i.
+int paged_device(int *sms) {
+  static std::atomic<int> seen[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  *sms = dev < 64 ? seen[dev].load(std::memory_order_relaxed) : 0;
+  if (*sms == 0) {
+    if (sm_count(sms)) return -1;
+    if (dev < 64) seen[dev].store(*sms, std::memory_order_relaxed);
+  }
+  return dev;
+}
+
+template <typename Kernel>
+int allow_smem(Kernel kern, int smem, int dev, std::atomic<uint64_t> &done) {
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit & done.load(std::memory_order_relaxed)) return SWA_OK;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return SWA_ERR_CUDA;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return SWA_OK;
+}
+
 // Runs that a paged attention call can split into: a bound that does not depend
 // on the device, so that a workspace has one size (148 SMs on a B200).
 constexpr int kPagedRuns = 148;
@@ -875,12 +900,11 @@ struct DecodePagedWorkspace {
 
 template <int D>
 int launch_paged_decode(const CUtensorMap &tk, const CUtensorMap &tv,
-                        const swa::PagedDecodeParams &p, int grid, cudaStream_t st) {
+                        const swa::PagedDecodeParams &p, int dev, int grid, cudaStream_t st) {
   using L = swa::PagedDecodeLayout<D>;
   auto kern = swa::paged_decode_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) !=
-      cudaSuccess)
-    return SWA_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (int e = allow_smem(kern, L::ALLOC, dev, done)) return e;
   kern<<<grid, swa::kPDThreads, L::ALLOC, st>>>(tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
   return launch_dependent(swa::paged_decode_merge_kernel<D>, dim3(grid), 128, p, st);
@@ -899,12 +923,11 @@ struct ChunkPagedWorkspace {
 
 template <int D>
 int launch_paged_fwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                     const swa::PagedFwdParams &p, int grid, cudaStream_t st) {
+                     const swa::PagedFwdParams &p, int dev, int grid, cudaStream_t st) {
   using L = swa::PagedFwdLayout<D>;
   auto kern = swa::paged_fwd_kernel<D>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::ALLOC) !=
-      cudaSuccess)
-    return SWA_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (int e = allow_smem(kern, L::ALLOC, dev, done)) return e;
   static std::atomic<int> launch_regs{-1};
   if (int e = check_launch_regs(kern, launch_regs)) return e;
   kern<<<grid, swa::kFwd2Threads, L::ALLOC, st>>>(tq, tk, tv, p);
@@ -1032,12 +1055,13 @@ int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int6
   const int64_t keys = W < p.c.max_pos ? W : p.c.max_pos;
   const int64_t tiles = slots * (keys / kBK + 4);
   int sms = 0;
-  if (sm_count(&sms)) return SWA_ERR_CUDA;
+  const int dev = paged_device(&sms);
+  if (dev < 0) return SWA_ERR_CUDA;
   int grid = sms < kPagedRuns ? sms : kPagedRuns;
   if (tiles < grid) grid = static_cast<int>(tiles);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_paged_fwd<128>(tq, tk, tv, p, grid, st)
-                  : launch_paged_fwd<64>(tq, tk, tv, p, grid, st);
+  return d == 128 ? launch_paged_fwd<128>(tq, tk, tv, p, dev, grid, st)
+                  : launch_paged_fwd<64>(tq, tk, tv, p, dev, grid, st);
 }
 
 int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int64_t *pos,
@@ -1078,12 +1102,13 @@ int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int
   const int64_t keys = W < p.c.max_pos ? W : p.c.max_pos;
   const int64_t tiles = static_cast<int64_t>(B) * Hkv * p.HB * (keys / swa::kPDKeys + 3);
   int sms = 0;
-  if (sm_count(&sms)) return SWA_ERR_CUDA;
+  const int dev = paged_device(&sms);
+  if (dev < 0) return SWA_ERR_CUDA;
   int grid = sms < kPagedRuns ? sms : kPagedRuns;
   if (tiles < grid) grid = static_cast<int>(tiles);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return d == 128 ? launch_paged_decode<128>(tk, tv, p, grid, st)
-                  : launch_paged_decode<64>(tk, tv, p, grid, st);
+  return d == 128 ? launch_paged_decode<128>(tk, tv, p, dev, grid, st)
+                  : launch_paged_decode<64>(tk, tv, p, dev, grid, st);
 }
 
 }  // extern "C"
