@@ -898,6 +898,22 @@ struct DecodePagedWorkspace {
   }
 };
 
+// Up to here a CTA per token is faster, beyond a warp per token (512 tokens 5.2 against
+// 7.3 us, 1024 tokens 9.3 against 8.2).
+constexpr int64_t kAppendFewTokens = 768;
+
+template <int D>
+int launch_append(bool interleaved, const swa::AppendParams &p, cudaStream_t st) {
+  const bool few = p.total <= kAppendFewTokens;
+  auto kern = interleaved ? (few ? swa::paged_append_kernel<D, true, swa::kAppendThreads>
+                                 : swa::paged_append_kernel<D, true, 32>)
+                          : (few ? swa::paged_append_kernel<D, false, swa::kAppendThreads>
+                                 : swa::paged_append_kernel<D, false, 32>);
+  const int64_t per = few ? 1 : swa::kAppendThreads / 32;
+  kern<<<static_cast<unsigned>((p.total + per - 1) / per), swa::kAppendThreads, 0, st>>>(p);
+  return check_launch();
+}
+
 template <int D>
 int launch_paged_decode(const CUtensorMap &tk, const CUtensorMap &tv,
                         const swa::PagedDecodeParams &p, int dev, int grid, cudaStream_t st) {
@@ -992,13 +1008,8 @@ int swa_paged_append(const void *k_new, int64_t k_new_stride, const void *v_new,
   p.Hkv = Hkv;
   p.zero_rest = zero_rest;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  auto kern = rotation && rotation->interleaved
-                  ? (d == 128 ? swa::paged_append_kernel<128, true>
-                              : swa::paged_append_kernel<64, true>)
-                  : (d == 128 ? swa::paged_append_kernel<128, false>
-                              : swa::paged_append_kernel<64, false>);
-  kern<<<static_cast<unsigned>(total), swa::kAppendThreads, 0, st>>>(p);
-  return check_launch();
+  const bool inter = rotation && rotation->interleaved;
+  return d == 128 ? launch_append<128>(inter, p, st) : launch_append<64>(inter, p, st);
 }
 
 size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d) {

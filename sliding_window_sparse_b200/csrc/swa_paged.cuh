@@ -22,10 +22,15 @@ struct PagedCache {
 
 // ------------------------------------------------------------------ append
 //
-// One token per CTA.  Bound: bytes (every input row read once, every output
-// row written once); a step of few tokens is bound by the chain of dependent
-// loads offsets -> start -> table entry, so the token's rows are loaded into
-// registers before that chain starts and wait for nothing.
+// One token per team: a warp, or the whole CTA where a call has so few tokens that
+// the latency of one counts.  Bound: bytes (every input row read once, every output
+// row written once), then, for few tokens, the chain of dependent loads offsets ->
+// start -> table entry; the token's first rows are loaded into registers before
+// that chain starts.  Measured with H = 32, Hkv = 8, d = 128: 64 tokens 3.9 us (a
+// warp each: 7.0), 512 tokens 5.2 (7.3), 1024 tokens 9.3 as CTAs and 8.2 as warps;
+// 9843 tokens 46 us (53 as CTAs), 5.3 TB/s; 16384 tokens with Hkv = 32 141 us, 5.7
+// TB/s.  Five items in flight per thread: with four the last takes 155 us, with six
+// (80 registers) 4096 tokens take 24 instead of 20 us.
 //
 // The rotation of pair i turns (x, y) by a = position * inv_freq[i].  In 32
 // bits a would lose its fraction of a turn for far positions (position 10^5,
@@ -34,7 +39,7 @@ struct PagedCache {
 // only the remainder in [-1/2, 1/2] goes to the 32-bit sincospi.  One angle
 // per pair and token serves all H + Hkv heads through shared memory.
 constexpr int kAppendThreads = 128;
-constexpr int kAppendBatch = 4;  // 16-element items a thread keeps in flight
+constexpr int kAppendBatch = 5;  // 16-element items a thread keeps in flight
 
 struct AppendParams {
   const __nv_bfloat16 *k_new, *v_new, *q;
@@ -53,14 +58,29 @@ struct AppendParams {
   int rot, n_axes;
 };
 
+// The number of threads of a team (the warp, or the CTA) for which `c` holds.
+template <int TEAM>
+__device__ __forceinline__ int team_count(bool c) {
+  return TEAM == 32 ? __popc(__ballot_sync(0xffffffffu, c)) : __syncthreads_count(c);
+}
+template <int TEAM>
+__device__ __forceinline__ void team_sync() {
+  if (TEAM == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
 // The number of i in [0, n] with cu[i] <= t, for non-decreasing cu (any value
-// in range otherwise): each round narrows the range by the CTA's thread count.
-__device__ __forceinline__ int64_t block_count_le(const int64_t *cu, int64_t n, int64_t t) {
+// in range otherwise): each round narrows the range by the team's size.
+template <int TEAM>
+__device__ __forceinline__ int64_t team_count_le(const int64_t *cu, int64_t n, int64_t t,
+                                                 int rank) {
   int64_t lo = 0, len = n + 1;
   while (len > 0) {
-    const int64_t step = (len + blockDim.x - 1) / blockDim.x;
-    const int64_t i = lo + (threadIdx.x + 1) * step - 1;
-    const int c = __syncthreads_count(i < lo + len && cu[i] <= t);
+    const int64_t step = (len + TEAM - 1) / TEAM;
+    const int64_t i = lo + (rank + 1) * step - 1;
+    const int c = team_count<TEAM>(i < lo + len && cu[i] <= t);
     const int64_t end = lo + len;
     lo += c * step;
     len = step - 1 < end - lo ? step - 1 : end - lo;
@@ -74,12 +94,14 @@ __device__ __forceinline__ void rotate_pair(float &x, float &y, float2 cs) {
   x = a;
 }
 
-template <int D, bool INTERLEAVED>
+template <int D, bool INTERLEAVED, int TEAM>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const AppendParams p) {
   constexpr int IPR = D / 16;  // items per row
-  __shared__ float2 s_cs[D / 2];
-  const int64_t t = blockIdx.x;
-  const int tid = threadIdx.x;
+  __shared__ float2 s_turn[kAppendThreads / TEAM][D / 2];
+  float2 *s_cs = s_turn[threadIdx.x / TEAM];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kAppendThreads / TEAM) + threadIdx.x / TEAM;
+  const int tid = threadIdx.x % TEAM;
+  if (t >= p.total) return;
   const int rows = p.H + 2 * p.Hkv, n_items = rows * IPR;
   const int rot16 = p.rot / 16;
   // Item i of a row is two 16-byte pieces: elements [8i, 8i+8) and their
@@ -101,7 +123,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   auto load = [&](int base) {
 #pragma unroll
     for (int u = 0; u < kAppendBatch; ++u) {
-      const int item = base + u * kAppendThreads + tid;
+      const int item = base + u * TEAM + tid;
       if (item >= n_items) break;
       int row, i, e0, e1;
       bool turns;
@@ -113,13 +135,13 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   };
   load(0);
 
-  if (blockIdx.x == 0) {  // offsets out of order or range: flagged once
-    for (int64_t i = tid; i < p.n_seq; i += kAppendThreads)
+  if (t == 0) {  // offsets out of order or range: flagged once
+    for (int64_t i = tid; i < p.n_seq; i += TEAM)
       if (p.cu_seqlens[i] < 0 || p.cu_seqlens[i + 1] < p.cu_seqlens[i] ||
           p.cu_seqlens[i + 1] > p.total)
         atomicOr(&g_swa_status, SWA_DEV_BADARG);
   }
-  const int64_t seq = block_count_le(p.cu_seqlens, p.n_seq, t) - 1;
+  const int64_t seq = team_count_le<TEAM>(p.cu_seqlens, p.n_seq, t, tid) - 1;
   int64_t pos = 0;
   int page = -1;
   if (seq >= 0 && seq < p.n_seq) {
@@ -135,17 +157,17 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
   }
   if (page < 0) {  // no slot to write
     if (p.zero_rest)
-      for (int i = tid; i < p.H * (D / 8); i += kAppendThreads)
+      for (int i = tid; i < p.H * (D / 8); i += TEAM)
         *reinterpret_cast<uint4 *>(p.q_out + t * p.qo_stride + 8 * i) = make_uint4(0, 0, 0, 0);
     return;
   }
   const int64_t slot =
       static_cast<int64_t>(page) * p.c.page_stride + (pos % p.c.page_size) * p.c.slot_stride;
 
-  if (tid < p.rot / 2) {
+  for (int pair = tid; pair < p.rot / 2; pair += TEAM) {
     int64_t at = pos;
     if (p.positions) {
-      int axis = p.pair_axis ? p.pair_axis[tid] : 0;
+      int axis = p.pair_axis ? p.pair_axis[pair] : 0;
       if (axis < 0 || axis >= p.n_axes) {
         atomicOr(&g_swa_status, SWA_DEV_BADARG);
         axis = 0;
@@ -153,19 +175,19 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
       at = p.positions[axis * p.pos_stride + t];
     }
     const double kInv2Pi = 0.15915494309189533577;
-    double turns = static_cast<double>(at) * (static_cast<double>(p.inv_freq[tid]) * kInv2Pi);
+    double turns = static_cast<double>(at) * (static_cast<double>(p.inv_freq[pair]) * kInv2Pi);
     turns -= rint(turns);
     float s, c;
     sincospif(static_cast<float>(2.0 * turns), &s, &c);
-    s_cs[tid] = make_float2(c, s);
+    s_cs[pair] = make_float2(c, s);
   }
-  __syncthreads();
+  team_sync<TEAM>();
 
-  for (int base = 0; base < n_items; base += kAppendBatch * kAppendThreads) {
+  for (int base = 0; base < n_items; base += kAppendBatch * TEAM) {
     if (base > 0) load(base);
 #pragma unroll
     for (int u = 0; u < kAppendBatch; ++u) {
-      const int item = base + u * kAppendThreads + tid;
+      const int item = base + u * TEAM + tid;
       if (item >= n_items) break;
       int row, i, e0, e1;
       bool turns;

@@ -93,12 +93,12 @@ struct DecodeRun {
   int b, kh;      // sequence, kvh * HB + head block
   int t0, t1;     // tiles of the unit in this run
   PagedSpan s;
-  __device__ __forceinline__ bool begin(const PagedDecodeParams &p, int b0, int64_t skip,
-                                        int64_t len) {
+  __device__ __forceinline__ bool begin(const PagedDecodeParams &p, int b0, int64_t pos0,
+                                        int64_t skip, int64_t len) {
     left = len;
     if (left <= 0) return false;
     b = b0;
-    s.init(decode_pos(p, b), p.W, p.n_sink);
+    s.init(pos0, p.W, p.n_sink);
     kh = static_cast<int>(skip / s.n);
     t0 = static_cast<int>(skip % s.n);
     t1 = left < s.n - t0 ? t0 + static_cast<int>(left) : s.n;
@@ -153,9 +153,10 @@ __global__ void __launch_bounds__(kPDThreads, 1)
   const uint32_t BAR_F = base + L::OFF_BAR, BAR_E = BAR_F + 8 * ST;
   float *s_red = reinterpret_cast<float *>(gbase + L::OFF_RED);
   float2 *s_ml = reinterpret_cast<float2 *>(gbase + L::OFF_ML);
-  int64_t *s_run = reinterpret_cast<int64_t *>(gbase + L::OFF_MISC);  // b0, tiles to skip
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_MISC + 16);
-  uint8_t *s_failed = gbase + L::OFF_MISC + 24;  // [8]
+  int64_t *s_run = reinterpret_cast<int64_t *>(gbase + L::OFF_MISC);  // b0, its pos, tiles
+                                                                        // to skip
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_MISC + 24);
+  uint8_t *s_failed = gbase + L::OFF_MISC + 32;  // [8]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x, units_per_seq = p.Hkv * p.HB;
 
@@ -207,11 +208,13 @@ __global__ void __launch_bounds__(kPDThreads, 1)
     if (hi > lo && lo >= at && lo < at + sum) {
       for (int b = b_lo; b < b_hi; ++b) {
         PagedSpan s;
-        s.init(decode_pos(p, b), p.W, p.n_sink);
+        const int64_t pos = decode_pos(p, b);
+        s.init(pos, p.W, p.n_sink);
         const int64_t n = static_cast<int64_t>(s.n) * units_per_seq;
         if (lo < at + n) {
           s_run[0] = b;
-          s_run[1] = lo - at;
+          s_run[1] = pos;
+          s_run[2] = lo - at;
           break;
         }
         at += n;
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kPDThreads, 1)
     __syncthreads();
   }
   const int b0 = static_cast<int>(s_run[0]);
-  const int64_t skip = s_run[1], len = hi - lo;
+  const int64_t pos0 = s_run[1], skip = s_run[2], len = hi - lo;
 
   if (warp == kPDWarps) {
     // ------------------------------------------------------------------ producer
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(kPDThreads, 1)
     DecodeRun r;
     int it = 0;
     bool ok = true;
-    for (bool more = r.begin(p, b0, skip, len); more && ok; more = r.next(p)) {
+    for (bool more = r.begin(p, b0, pos0, skip, len); more && ok; more = r.next(p)) {
       const int32_t *row = p.c.table + r.b * p.c.table_stride;
       const int head = r.kh / p.HB;
       // this lane's box of tile i: its page and first slot (-1: no visible key lies there)
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kPDThreads, 1)
   DecodeRun r;
   int it = 0;
   int2 split = make_int2(-1, 0);  // the unit to be joined by the merge kernel's block of this run
-  for (bool more = r.begin(p, b0, skip, len); more; more = r.next(p)) {
+  for (bool more = r.begin(p, b0, pos0, skip, len); more; more = r.next(p)) {
     bool ok = true;
     const int kvh = r.kh / p.HB, hb = r.kh % p.HB;
     const int rows = min(kPDRows, p.G - hb * kPDRows);
@@ -510,24 +513,40 @@ __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const PagedDeco
   const int64_t h0 = static_cast<int64_t>(b) * p.H + kvh * p.G + hb * kPDRows;
   for (int e = threadIdx.x; e < rows * (D / 4); e += blockDim.x) {
     const int row = e / (D / 4), col = (e % (D / 4)) * 4;
-    float M = -INFINITY;
-#pragma unroll 4
-    for (int j = c; j < end; ++j)
-      M = fmaxf(M, p.ws_ml[(j == c ? 2 * c + 1 : 2 * j) * kPDRows + row].x);
+    // eight parts in flight at a time, their maximum joined to the running one
+    constexpr int N = 8;
+    float M = -INFINITY, Ls = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float Ls = 0.f;
-#pragma unroll 4
-    for (int j = c; j < end; ++j) {
-      const int slot = j == c ? 2 * c + 1 : 2 * j;
-      const float2 ml = p.ws_ml[slot * kPDRows + row];
-      const float w = ex2(ml.x - M);  // every part has a visible key: both are finite
-      const float4 v = *reinterpret_cast<const float4 *>(
-          p.ws_o + (static_cast<int64_t>(slot) * kPDRows + row) * D + col);
-      Ls = fmaf(ml.y, w, Ls);
-      a.x = fmaf(v.x, w, a.x);
-      a.y = fmaf(v.y, w, a.y);
-      a.z = fmaf(v.z, w, a.z);
-      a.w = fmaf(v.w, w, a.w);
+    for (int j0 = c; j0 < end; j0 += N) {
+      float2 ml[N];
+      float4 v[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int j = j0 + k, slot = j == c ? 2 * c + 1 : 2 * j;
+        ml[k] = make_float2(-INFINITY, 0.f);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < end) {
+          ml[k] = p.ws_ml[slot * kPDRows + row];
+          v[k] = *reinterpret_cast<const float4 *>(
+              p.ws_o + (static_cast<int64_t>(slot) * kPDRows + row) * D + col);
+        }
+      }
+      float mn = M;
+#pragma unroll
+      for (int k = 0; k < N; ++k) mn = fmaxf(mn, ml[k].x);  // part c has a key: finite
+      const float w0 = ex2(M - mn);
+      Ls *= w0;
+      a = make_float4(a.x * w0, a.y * w0, a.z * w0, a.w * w0);
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const float w = ex2(ml[k].x - mn);
+        Ls = fmaf(ml[k].y, w, Ls);
+        a.x = fmaf(v[k].x, w, a.x);
+        a.y = fmaf(v[k].y, w, a.y);
+        a.z = fmaf(v[k].z, w, a.z);
+        a.w = fmaf(v[k].w, w, a.w);
+      }
+      M = mn;
     }
     const float inv = 1.f / Ls;
     *reinterpret_cast<uint2 *>(p.out + (h0 + row) * D + col) =
