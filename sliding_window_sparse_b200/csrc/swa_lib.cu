@@ -926,6 +926,12 @@ int launch_paged_decode(const CUtensorMap &tk, const CUtensorMap &tv,
   return launch_dependent(swa::paged_decode_merge_kernel<D>, dim3(grid), 128, p, st);
 }
 
+swa::FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while ((uint64_t(1) << l) < d) ++l;
+  return {static_cast<uint32_t>(((uint64_t(1) << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 struct ChunkPagedWorkspace {
   size_t run, ml, o, bytes;
   explicit ChunkPagedWorkspace(int d) {
@@ -1046,6 +1052,8 @@ int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int6
   p.G = H / Hkv;
   p.tpt = kBQ / p.G;
   p.g_inv = ((1 << 16) + p.G - 1) / p.G;
+  p.by_hkv = fast_div(Hkv);
+  p.by_tu = fast_div(2 * p.tpt);
   const int64_t slots = (total / (2 * p.tpt) + n_seq) * Hkv;
   if (slots > (1 << 30)) return SWA_ERR_UNSUPPORTED;
   p.n_slots = static_cast<int>(slots);

@@ -52,6 +52,15 @@ namespace swa {
 constexpr int kUnitCost = 1;   // of a unit besides its key tiles, in key tiles
 constexpr int kUnitRing = 4;   // units the scheduler is ahead
 
+// n / d for n < 2^31 by a multiplication: mul = ceil(2^(31 + l) / d), l = ceil(log2 d),
+// shift = 31 + l (the excess of mul adds n / 2^31 < 1 parts of 1 / d at most).
+struct FastDiv {
+  uint32_t mul, shift;
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * mul) >> shift);
+  }
+};
+
 struct PagedFwdParams {
   __nv_bfloat16 *out;  // [total, H, D]
   float *lse;          // [H, total] or nullptr
@@ -62,6 +71,7 @@ struct PagedFwdParams {
   int H, Hkv, G;
   int tpt;       // tokens per tile: 128 / G
   int g_inv;     // ceil(2^16 / G): r * g_inv >> 16 = r / G for r < 128
+  FastDiv by_hkv, by_tu;  // divisions by Hkv and by a unit's 2 tpt tokens
   int n_slots;   // entries of the unit list, empty ones among them
   int W;         // clamped below 2^31 - 1024
   int n_sink, zero_rest;
@@ -129,42 +139,37 @@ struct PagedUnit {
 // Entry u of the unit list: sequence b owns the entries from base(b) * Hkv on, with
 // base(b) = cu[b] / (tokens per unit) + b, which leaves room for its units on every
 // key/value head without a sum over the sequences before it; what is left over
-// is empty.  Returns the unit's key tiles (0: an empty entry).
+// is empty.  Sets b .. qpos and n and returns n, the unit's key tiles (0: an empty entry).
 __device__ __forceinline__ int paged_unit(const PagedFwdParams &p, int u, PagedUnit &U) {
   if (u >= p.n_slots) return 0;
-  const unsigned tu = 2 * p.tpt, q = static_cast<unsigned>(u) / p.Hkv;
-  auto offset = [&](int b) -> unsigned {  // in range, whatever the array holds
-    const int64_t v = p.cu_seqlens[b];
-    return v < 0 ? 0u : (v > p.total ? static_cast<unsigned>(p.total) : static_cast<unsigned>(v));
-  };
-  int lo = -1, hi = p.n_seq;  // the last sequence whose base is <= q
+  const int tu = 2 * p.tpt;
+  const uint32_t q = p.by_hkv(u);
+  int lo = 0, hi = p.n_seq;  // the last sequence whose base is <= q, from the first on
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    // cu / tu + mid <= q
-    if (static_cast<int64_t>(offset(mid)) <
-        (static_cast<int64_t>(q) - mid + 1) * static_cast<int64_t>(tu))
+    // cu / tu + mid <= q  (for any cu the search stays in range)
+    if (p.cu_seqlens[mid] < (static_cast<int64_t>(q) - mid + 1) * tu)
       lo = mid;
     else
       hi = mid;
   }
-  if (lo < 0) return 0;
   const int64_t a = p.cu_seqlens[lo], e = p.cu_seqlens[lo + 1], s = p.q_start[lo];
   if (a < 0 || e <= a || e > p.total || s < 0 || s + (e - a) > p.c.max_pos) return 0;
-  const unsigned b0 = static_cast<unsigned>(a) / tu + lo;
-  const unsigned per = static_cast<unsigned>(e) / tu + lo + 1 - b0;
-  const unsigned rem = u - b0 * p.Hkv, kvh = rem / per, tok = (rem - kvh * per) * tu;
-  const unsigned len = static_cast<unsigned>(e - a);
-  if (kvh >= static_cast<unsigned>(p.Hkv) || tok >= len) return 0;
+  const uint32_t b0 = p.by_tu(static_cast<uint32_t>(a)) + lo;
+  if (q < b0) return 0;
+  const uint32_t per = p.by_tu(static_cast<uint32_t>(e)) + lo + 1 - b0;
+  const uint32_t rem = u - b0 * p.Hkv, kvh = rem / per, tok = (rem - kvh * per) * tu;
+  const uint32_t len = static_cast<uint32_t>(e - a);
+  if (kvh >= static_cast<uint32_t>(p.Hkv) || tok >= len) return 0;
   U.b = lo;
   U.kvh = static_cast<int>(kvh);
   U.tok = static_cast<int>(a) + static_cast<int>(tok);
-  U.ntok = static_cast<int>(len - tok < tu ? len - tok : tu);
+  U.ntok = min(static_cast<int>(len - tok), tu);
   U.qpos = static_cast<int>(s) + static_cast<int>(tok);
   const int low = U.qpos - p.W + 1 > 0 ? U.qpos - p.W + 1 : 0, first = low / kKT;
   U.n = (U.qpos + U.ntok - 1) / kKT - first + 1 + (p.n_sink > 0 && first > 0 ? 1 : 0);
   return U.n;
 }
-
 template <int D>
 __global__ void __launch_bounds__(kFwd2Threads, 1)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -235,12 +240,12 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   // the matrix of units.  Every CTA sums the costs, a contiguous piece per thread.
   const int n_cols = gridDim.x, n_rows = (p.n_slots + n_cols - 1) / n_cols;
   const int n_list = n_rows * n_cols;
-  auto unit_at = [&](int s, PagedUnit &U) -> int {
+  auto entry = [&](int s) -> int {
     const int col = s / n_rows;
-    return paged_unit(p, (s - col * n_rows) * n_cols + col, U);
+    return (s - col * n_rows) * n_cols + col;
   };
   int64_t T = 0, lo, hi;
-  int P;
+  int P = 0;
   {
     if (blockIdx.x == 0)  // sequences that are skipped
       for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads) {
@@ -252,40 +257,44 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
     const int per = (n_list + kFwd2Threads - 1) / kFwd2Threads;
     const int s_lo = min(static_cast<int>(threadIdx.x) * per, n_list);
     const int s_hi = min(s_lo + per, n_list);
-    int64_t sum = 0;
-    for (int s = s_lo; s < s_hi; ++s) {
-      PagedUnit U;
-      const int n = unit_at(s, U);
-      sum += n ? n + kUnitCost : 0;
-    }
-    int64_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    int64_t at = incl - sum;
-    for (int w = 0; w < kFwd2Threads / 32; ++w) {
-      if (w < warp) at += s_warp[w];
-      T += s_warp[w];
-    }
-    const int c = blockIdx.x;
-    P = T < n_cols ? static_cast<int>(T) : n_cols;
-    lo = c < P ? T * c / P : 0;
-    hi = c < P ? T * (c + 1) / P : 0;
-    if (hi > lo && lo >= at && lo < at + sum) {
-      for (int s = s_lo; s < s_hi; ++s) {
-        PagedUnit U;
-        const int n = unit_at(s, U);
-        if (n && lo < at + n + kUnitCost) {
-          s_run[0] = s;
-          s_run[1] = at;
-          break;
+    // Two passes over one piece of code, which a launch meets cold: the sums, then the
+    // entry in which this run begins.
+    int64_t sum = 0, at = 0;
+    lo = hi = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (pass == 0 || (hi > lo && lo >= at && lo < at + sum)) {
+        int64_t acc = at;
+        for (int s = s_lo; s < s_hi; ++s) {
+          PagedUnit U;
+          const int n = paged_unit(p, entry(s), U), cost = n ? n + kUnitCost : 0;
+          if (pass && lo < acc + cost) {
+            s_run[0] = s;
+            s_run[1] = acc;
+            break;
+          }
+          acc += cost;
         }
-        at += n ? n + kUnitCost : 0;
+        if (pass == 0) sum = acc;
       }
+      if (pass) break;
+      int64_t incl = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) s_warp[warp] = incl;
+      __syncthreads();
+      at = incl - sum;
+      for (int w = 0; w < kFwd2Threads / 32; ++w) {
+        if (w < warp) at += s_warp[w];
+        T += s_warp[w];
+      }
+      const int c = blockIdx.x;
+      P = T < n_cols ? static_cast<int>(T) : n_cols;
+      lo = c < P ? T * c / P : 0;
+      hi = c < P ? T * (c + 1) / P : 0;
     }
   }
   tc_fence_before();
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         int64_t at = s_run[1];
         while (ok && at < hi && s < n_list) {
           PagedUnit U;
-          const int n = s + lane < n_list ? unit_at(s + lane, U) : 0;
+          const int n = s + lane < n_list ? paged_unit(p, entry(s + lane), U) : 0;
           const int cost = n ? n + kUnitCost : 0;
           int incl = cost;
 #pragma unroll
