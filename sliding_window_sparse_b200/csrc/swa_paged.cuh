@@ -20,6 +20,13 @@ struct PagedCache {
   int64_t max_pos = 0;  // positions a table row can map: max_pages * page_size
 };
 
+// T c / P of a run's border; in 32 bits (a 64-bit division takes 500 cycles of a
+// launch's start) unless the list is very long.
+__device__ __forceinline__ int64_t mul_div(int64_t T, int c, int P) {
+  if (T < (1 << 22)) return static_cast<uint32_t>(T) * static_cast<uint32_t>(c) / P;
+  return T * c / P;
+}
+
 // ------------------------------------------------------------------ append
 //
 // One token per team: a warp, or the whole CTA where a call has so few tokens that

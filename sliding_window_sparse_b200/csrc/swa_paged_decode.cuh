@@ -99,8 +99,9 @@ struct DecodeRun {
     if (left <= 0) return false;
     b = b0;
     s.init(pos0, p.W, p.n_sink);
-    kh = static_cast<int>(skip / s.n);
-    t0 = static_cast<int>(skip % s.n);
+    kh = skip < (int64_t(1) << 32) ? static_cast<int>(static_cast<uint32_t>(skip) / s.n)
+                                   : static_cast<int>(skip / s.n);
+    t0 = static_cast<int>(skip - static_cast<int64_t>(kh) * s.n);
     t1 = left < s.n - t0 ? t0 + static_cast<int>(left) : s.n;
     return true;
   }
@@ -202,8 +203,8 @@ __global__ void __launch_bounds__(kPDThreads, 1)
       total += s_warp[w];
     }
     P = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
-    lo = cta < P ? total * cta / P : 0;
-    hi = cta < P ? total * (cta + 1) / P : 0;
+    lo = cta < P ? mul_div(total, cta, P) : 0;
+    hi = cta < P ? mul_div(total, cta + 1, P) : 0;
     int64_t at = before + incl - sum;
     if (hi > lo && lo >= at && lo < at + sum) {
       for (int b = b_lo; b < b_hi; ++b) {

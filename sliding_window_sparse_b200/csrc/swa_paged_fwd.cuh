@@ -258,16 +258,33 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
     const int s_lo = min(static_cast<int>(threadIdx.x) * per, n_list);
     const int s_hi = min(s_lo + per, n_list);
     // Two passes over one piece of code, which a launch meets cold: the sums, then the
-    // entry in which this run begins.
+    // entry in which this run begins (by the costs that the first pass left in shared
+    // memory, as far as the K and V stages hold them).
+    int *s_cost = reinterpret_cast<int *>(gbase + L::OFF_K);
+    const bool stored = n_list <= static_cast<int>((NK + NV) * L::KV_BYTES / 4);
+    const int col0 = s_lo / n_rows, row0 = s_lo - col0 * n_rows;
     int64_t sum = 0, at = 0;
     lo = hi = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
       if (pass == 0 || (hi > lo && lo >= at && lo < at + sum)) {
         int64_t acc = at;
+        int col = col0, row = row0;
+#pragma unroll 1
         for (int s = s_lo; s < s_hi; ++s) {
-          PagedUnit U;
-          const int n = paged_unit(p, entry(s), U), cost = n ? n + kUnitCost : 0;
+          int cost;
+          if (pass && stored) {
+            cost = s_cost[s];
+          } else {
+            PagedUnit U;
+            const int n = paged_unit(p, row * n_cols + col, U);
+            cost = n ? n + kUnitCost : 0;
+            if (stored) s_cost[s] = cost;
+            if (++row == n_rows) {
+              row = 0;
+              ++col;
+            }
+          }
           if (pass && lo < acc + cost) {
             s_run[0] = s;
             s_run[1] = acc;
@@ -293,8 +310,8 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       }
       const int c = blockIdx.x;
       P = T < n_cols ? static_cast<int>(T) : n_cols;
-      lo = c < P ? T * c / P : 0;
-      hi = c < P ? T * (c + 1) / P : 0;
+      lo = c < P ? mul_div(T, c, P) : 0;
+      hi = c < P ? mul_div(T, c + 1, P) : 0;
     }
   }
   tc_fence_before();
@@ -596,10 +613,6 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
           const int64_t a = at + incl - cost;  // the unit's tiles are costs [a, a + n)
           U.t0 = lo - a <= 0 ? 0 : (lo - a < n ? static_cast<int>(lo - a) : n);
           U.t1 = hi - a <= 0 ? 0 : (hi - a < n ? static_cast<int>(hi - a) : n);
-          if (n && U.t0 == 0 && U.t1 > 0 && U.t1 < n)
-            // run j begins inside iff floor(T j / P) < a + n iff j < (a + n) P / T
-            p.ws_run[blockIdx.x] = make_int4(U.tok, U.kvh, U.ntok,
-                                             static_cast<int>(((a + n) * P + T - 1) / T));
           if (n) U.plan(p);
           uint32_t todo = __ballot_sync(0xffffffffu, n && U.t0 < U.t1);
           for (; todo && ok; todo &= todo - 1, ++it) {
@@ -607,6 +620,10 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             if (lane == i) ok = publish(U);
             ok = __shfl_sync(0xffffffffu, ok, i);
           }
+          if (n && U.t0 == 0 && U.t1 > 0 && U.t1 < n)
+            // run j begins inside iff floor(T j / P) < a + n iff j < (a + n) P / T
+            p.ws_run[blockIdx.x] = make_int4(U.tok, U.kvh, U.ntok,
+                                             static_cast<int>(((a + n) * P + T - 1) / T));
           at += __shfl_sync(0xffffffffu, incl, 31);
           s += 32;
         }
