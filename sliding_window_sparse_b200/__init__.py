@@ -20,7 +20,6 @@ page_size, d]`` tensors of any strides (a token-major cache is passed as
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -460,27 +459,32 @@ def swa_ring_slot_positions(n_written, W: int, out=None):
     return out
 
 
-# The paged calls serve single tokens, where the host's time counts: their checks ask each tensor
-# once, and the stream comes without a Python object around it (2 us).
+# The paged calls serve single tokens, where the host's time counts: a check asks a tensor once
+# and names it only when it fails, and the stream comes without a Python object around it.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_bf16 = torch.bfloat16
 
 
-def _one_device(index, *named):
-    """All tensors on CUDA device `index`; a context in which it is the current one."""
-    for name, t in named:
+def _elsewhere(index, **named):
+    """Raises for the first tensor that is not on CUDA device `index`."""
+    for name, t in named.items():
         if t is not None and t.get_device() != index:
             raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
-    return (_CURRENT if torch.cuda.current_device() == index else torch.cuda.device(index))
 
 
-_CURRENT = contextlib.nullcontext()
+def _on(index, call, *args):
+    """call(*args, stream) with CUDA device `index` current."""
+    if torch.cuda.current_device() == index:
+        return call(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return call(*args, _raw_stream(index))
 
 
 def _need_rows(t, name, shape):
     """bf16 [tokens, heads, d] whose token rows may lie apart (a slice of a fused projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda or t.dtype != torch.bfloat16 or t.shape != shape:
+    if not t.is_cuda or t.dtype is not _bf16 or t.shape != shape:
         raise ValueError(f"{name} must be a bfloat16 CUDA tensor of shape {list(shape)}, got "
                          f"{t.dtype} {list(t.shape)} on {t.device}")
     total, heads, d = shape
@@ -490,7 +494,16 @@ def _need_rows(t, name, shape):
     return apart if total > 1 else heads * d
 
 
-def _need_int(t, name, dtype, shape):
+def _need_list(t, name, dtype, length):
+    """A contiguous CUDA vector of `length` entries."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda or t.dtype is not dtype or t.shape != (length,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor [{length}], got "
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+
+
+def _need_like(t, name, dtype, shape):
     _need(t, name, dtype, len(shape))
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
@@ -498,35 +511,36 @@ def _need_int(t, name, dtype, shape):
 
 def _paged_cache(k_cache, v_cache, block_table, n_seq):
     """The cache's structure for the library, its heads and head dim."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{n} must be a torch.Tensor")
-        if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 4:
-            raise ValueError(f"{n} must be a bfloat16 CUDA tensor [n_pages, Hkv, page_size, d]")
+    if not (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor)
+            and isinstance(block_table, torch.Tensor)):
+        raise TypeError("k_cache, v_cache and block_table must be torch.Tensors")
     shape, strides = k_cache.shape, k_cache.stride()
+    if not k_cache.is_cuda or k_cache.dtype is not _bf16 or v_cache.dtype is not _bf16 or \
+            len(shape) != 4:
+        raise ValueError("k_cache and v_cache must be bfloat16 CUDA tensors "
+                         "[n_pages, Hkv, page_size, d]")
     n_pages, heads, page_size, d = shape
     same = v_cache.shape == shape and v_cache.stride() == strides
     if 1 in shape[:3]:
         # the stride of a dimension of one entry says nothing: any valid one will do
-        other = v_cache.stride()
         same = v_cache.shape == shape and all(n == 1 or a == b for n, a, b in
-                                              zip(shape, strides, other))
+                                              zip(shape, strides, v_cache.stride()))
         strides = [d if n == 1 else s for n, s in zip(shape[:3], strides)] + [strides[3]]
     if not same:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
     if strides[3] != 1:
         raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
-    if not isinstance(block_table, torch.Tensor):
-        raise TypeError("block_table must be a torch.Tensor")
-    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            block_table.shape[0] != n_seq or (block_table.shape[1] > 1 and
-                                              block_table.stride(1) != 1):
-        raise ValueError(f"block_table must be an int32 CUDA tensor [{n_seq}, max_pages], "
-                         "contiguous along a row")
-    max_pages = block_table.shape[1]
+    rows = block_table.shape
+    if not block_table.is_cuda or block_table.dtype is not torch.int32 or len(rows) != 2 or \
+            rows[0] != n_seq:
+        raise ValueError(f"block_table must be an int32 CUDA tensor [{n_seq}, max_pages]")
+    max_pages = rows[1]
+    apart, one = block_table.stride()
+    if one != 1 and max_pages > 1:
+        raise ValueError("block_table must be contiguous along a row")
     return (PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), strides[0],
                        strides[1], strides[2], n_pages, max_pages,
-                       block_table.stride(0) if n_seq > 1 else max_pages, page_size), heads, d)
+                       apart if n_seq > 1 else max_pages, page_size), heads, d)
 
 
 def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_start, q=None,
@@ -548,9 +562,9 @@ def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_
     total, Hkv, d = shape = k_new.shape
     ks = _need_rows(k_new, "k_new", shape)
     vs = _need_rows(v_new, "v_new", shape)
-    _need(cu_seqlens, "cu_seqlens", torch.int64, 1)
-    n_seq = cu_seqlens.shape[0] - 1
-    _need_int(q_start, "q_start", torch.int64, (n_seq,))
+    n_seq = q_start.shape[0] if isinstance(q_start, torch.Tensor) and q_start.dim() == 1 else 0
+    _need_list(q_start, "q_start", torch.int64, n_seq)
+    _need_list(cu_seqlens, "cu_seqlens", torch.int64, n_seq + 1)
     cache, heads, dk = _paged_cache(k_cache, v_cache, block_table, n_seq)
     if heads != Hkv or dk != d:
         raise ValueError(f"the cache has {heads} heads of {dk}, expected {Hkv} of {d}")
@@ -581,22 +595,26 @@ def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_
         if pair_axis is not None:
             if positions is None:
                 raise ValueError("pair_axis without positions")
-            _need_int(pair_axis, "pair_axis", torch.int32, (half,))
+            _need_list(pair_axis, "pair_axis", torch.int32, half)
         rotation = Rotation(_ptr(inv_freq), _ptr(positions), _ptr(pair_axis), total, 2 * half,
                             1 if interleaved else 0, n_axes)
     elif positions is not None or pair_axis is not None:
         raise ValueError("positions and pair_axis need inv_freq")
     index = k_new.get_device()
-    with _one_device(index, ("v_new", v_new), ("k_cache", k_cache), ("v_cache", v_cache),
-                     ("block_table", block_table), ("cu_seqlens", cu_seqlens),
-                     ("q_start", q_start), ("q", q), ("q_out", q_out), ("inv_freq", inv_freq),
-                     ("positions", positions), ("pair_axis", pair_axis)):
-        check("swa_paged_append",
-              lib().swa_paged_append(k_new.data_ptr(), ks, v_new.data_ptr(), vs, _ptr(q), qs,
-                                     _ptr(q_out), qos, ctypes.byref(cache),
-                                     ctypes.byref(rotation) if rotation else None,
-                                     cu_seqlens.data_ptr(), q_start.data_ptr(), n_seq, total, H,
-                                     Hkv, d, 1 if zero_rest else 0, _raw_stream(index)))
+    if not (v_new.get_device() == k_cache.get_device() == v_cache.get_device()
+            == block_table.get_device() == cu_seqlens.get_device() == q_start.get_device()
+            == index and (q is None or q.get_device() == q_out.get_device() == index)
+            and (rotation is None or inv_freq.get_device() == index)
+            and (positions is None or positions.get_device() == index)
+            and (pair_axis is None or pair_axis.get_device() == index)):
+        _elsewhere(index, v_new=v_new, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                   cu_seqlens=cu_seqlens, q_start=q_start, q=q, q_out=q_out, inv_freq=inv_freq,
+                   positions=positions, pair_axis=pair_axis)
+    check("swa_paged_append",
+          _on(index, lib().swa_paged_append, k_new.data_ptr(), ks, v_new.data_ptr(), vs, _ptr(q),
+              qs, _ptr(q_out), qos, ctypes.byref(cache),
+              ctypes.byref(rotation) if rotation else None, cu_seqlens.data_ptr(),
+              q_start.data_ptr(), n_seq, total, H, Hkv, d, 1 if zero_rest else 0))
     return q_out
 
 
@@ -615,10 +633,10 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
     of tokens outside every sequence keep what out and lse held (zeros when allocated here).
     """
     _need(q, "q", dims=3)
-    _need(cu_seqlens, "cu_seqlens", torch.int64, 1)
     total, H, d = q.shape
-    n_seq = cu_seqlens.shape[0] - 1
-    _need_int(q_start, "q_start", torch.int64, (n_seq,))
+    n_seq = q_start.shape[0] if isinstance(q_start, torch.Tensor) and q_start.dim() == 1 else 0
+    _need_list(q_start, "q_start", torch.int64, n_seq)
+    _need_list(cu_seqlens, "cu_seqlens", torch.int64, n_seq + 1)
     cache, Hkv, dk = _paged_cache(k_cache, v_cache, block_table, n_seq)
     if dk != d:
         raise ValueError(f"the cache has heads of {dk}, q of {d}")
@@ -630,30 +648,31 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
         if out.shape != q.shape:
             raise ValueError("out must match q")
     if lse is not None:
-        _need_int(lse, "lse", torch.float32, (H, total))
+        _need_like(lse, "lse", torch.float32, (H, total))
     index = q.get_device()
-    with _one_device(index, ("k_cache", k_cache), ("v_cache", v_cache),
-                     ("block_table", block_table), ("cu_seqlens", cu_seqlens),
-                     ("q_start", q_start), ("out", out), ("lse", lse), ("workspace", workspace)):
-        # what is allocated here is zeroed by the call outside the sequences, unless the other
-        # of the two is the caller's: then its rows stay, and ours are zeroed first
-        zero_rest = new_out and (new_lse or lse is None)
-        if new_out:
-            out = torch.empty_like(q) if zero_rest else torch.zeros_like(q)
-        if new_lse:
-            lse = q.new_empty((H, total), dtype=torch.float32)
-            if not zero_rest:
-                lse.zero_()
-        if workspace is None:
-            need = swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d)
-            workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
-        check("swa_attn_chunk_paged",
-              lib().swa_attn_chunk_paged(q.data_ptr(), ctypes.byref(cache), cu_seqlens.data_ptr(),
-                                         q_start.data_ptr(), out.data_ptr(), _ptr(lse), n_seq,
-                                         total, H, Hkv, d, W, n_sink, scale,
-                                         1 if zero_rest else 0, workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(),
-                                         _raw_stream(index)))
+    if not (k_cache.get_device() == v_cache.get_device() == block_table.get_device()
+            == cu_seqlens.get_device() == q_start.get_device() == index):
+        _elsewhere(index, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
+                   cu_seqlens=cu_seqlens, q_start=q_start)
+    if not (new_out and lse is None and workspace is None):
+        _elsewhere(index, out=out, lse=lse, workspace=workspace)
+    # what is allocated here is zeroed by the call outside the sequences, unless the other of
+    # the two is the caller's: then its rows stay, and ours are zeroed first
+    zero_rest = new_out and (new_lse or lse is None)
+    if new_out:
+        out = torch.empty_like(q) if zero_rest else torch.zeros_like(q)
+    if new_lse:
+        lse = q.new_empty((H, total), dtype=torch.float32)
+        if not zero_rest:
+            lse.zero_()
+    if workspace is None:
+        need = swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d)
+        workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
+    check("swa_attn_chunk_paged",
+          _on(index, lib().swa_attn_chunk_paged, q.data_ptr(), ctypes.byref(cache),
+              cu_seqlens.data_ptr(), q_start.data_ptr(), out.data_ptr(), _ptr(lse), n_seq, total,
+              H, Hkv, d, W, n_sink, scale, 1 if zero_rest else 0, workspace.data_ptr(),
+              workspace.numel() * workspace.element_size()))
     return (out, lse) if return_lse else out
 
 
@@ -671,7 +690,7 @@ def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
     """
     _need(q, "q", dims=3)
     B, H, d = q.shape
-    _need_int(pos, "pos", torch.int64, (B,))
+    _need_list(pos, "pos", torch.int64, B)
     cache, Hkv, dk = _paged_cache(k_cache, v_cache, block_table, B)
     if dk != d:
         raise ValueError(f"the cache has heads of {dk}, q of {d}")
@@ -682,24 +701,24 @@ def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
         if out.shape != q.shape:
             raise ValueError("out must match q")
     if lse is not None:
-        _need_int(lse, "lse", torch.float32, (B, H))
+        _need_like(lse, "lse", torch.float32, (B, H))
     index = q.get_device()
-    with _one_device(index, ("k_cache", k_cache), ("v_cache", v_cache),
-                     ("block_table", block_table), ("pos", pos), ("out", out), ("lse", lse),
-                     ("workspace", workspace)):
-        if out is None:
-            out = torch.empty_like(q)
-        if return_lse and lse is None:
-            lse = q.new_empty((B, H), dtype=torch.float32)
-        if workspace is None:
-            need = swa_decode_paged_workspace_bytes(B, H, Hkv, d)
-            workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
-        check("swa_attn_decode_paged",
-              lib().swa_attn_decode_paged(q.data_ptr(), ctypes.byref(cache), pos.data_ptr(),
-                                          out.data_ptr(), _ptr(lse), B, H, Hkv, d, W, n_sink,
-                                          scale, workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(),
-                                          _raw_stream(index)))
+    if not (k_cache.get_device() == v_cache.get_device() == block_table.get_device()
+            == pos.get_device() == index):
+        _elsewhere(index, k_cache=k_cache, v_cache=v_cache, block_table=block_table, pos=pos)
+    if not (out is None and lse is None and workspace is None):
+        _elsewhere(index, out=out, lse=lse, workspace=workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    if return_lse and lse is None:
+        lse = q.new_empty((B, H), dtype=torch.float32)
+    if workspace is None:
+        need = swa_decode_paged_workspace_bytes(B, H, Hkv, d)
+        workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
+    check("swa_attn_decode_paged",
+          _on(index, lib().swa_attn_decode_paged, q.data_ptr(), ctypes.byref(cache),
+              pos.data_ptr(), out.data_ptr(), _ptr(lse), B, H, Hkv, d, W, n_sink, scale,
+              workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     return (out, lse) if return_lse else out
 
 
