@@ -21,6 +21,7 @@ page_size, d]`` tensors of any strides (a token-major cache is passed as
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -618,6 +619,7 @@ def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_
     return q_out
 
 
+@functools.lru_cache(maxsize=256)
 def swa_chunk_paged_workspace_bytes(n_seq: int, total: int, H: int, Hkv: int, d: int) -> int:
     return int(lib().swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d))
 
@@ -676,6 +678,7 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
     return (out, lse) if return_lse else out
 
 
+@functools.lru_cache(maxsize=256)
 def swa_decode_paged_workspace_bytes(B: int, H: int, Hkv: int, d: int) -> int:
     return int(lib().swa_decode_paged_workspace_bytes(B, H, Hkv, d))
 

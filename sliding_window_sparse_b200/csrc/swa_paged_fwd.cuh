@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             b_ahead = true;
           }
           tc_commit(BAR_KE + 8 * (kv % NK));
-          bool first[2] = {true, true}, o_done[2] = {false, false};
+          bool first[2] = {true, true};
           bool stop = false;  // a wait gave up: issue nothing more
           while (have) {
             if (!has_next) tc_commit(BAR_QE);  // every S of this unit is issued
@@ -531,10 +531,9 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
                 break;
               }
               first[0] = false;
-              if (j - 1 == U.a_last) {
-                tc_commit(BAR_O);
-                o_done[0] = true;
-              }
+              // o_full completes once per unit in which the tile had work; its next
+              // completion needs that tile's softmax to hand over its next P
+              if (j - 1 == U.a_last) tc_commit(BAR_O);
             }
             if (has_next) {
               if (!k_wait(kv + 1)) {
@@ -549,10 +548,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
                 break;
               }
               first[1] = false;
-              if (j - 1 == U.b_last) {
-                tc_commit(BAR_O + 8);
-                o_done[1] = true;
-              }
+              if (j - 1 == U.b_last) tc_commit(BAR_O + 8);
             }
             tc_commit(BAR_VE + 8 * sv);  // V(j) is read by both PV MMAs
             if (has_next) {
@@ -569,10 +565,6 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             nb = has_next && U.live(1, j);
           }
           if (stop) break;
-          // o_full completes once per unit in which the tile had work; its next
-          // completion needs that tile's softmax to hand over its next P
-          if (!first[0] && !o_done[0]) tc_commit(BAR_O);
-          if (!first[1] && !o_done[1]) tc_commit(BAR_O + 8);
           ++q_iter;
         }
         // every MMA issued must complete before the tensor memory is freed
