@@ -534,8 +534,8 @@ SWA_API int swa_paged_append(const void *k_new, int64_t k_new_stride, const void
 /*
  * swa_chunk_paged_workspace_bytes, swa_decode_paged_workspace_bytes -- bytes
  * of scratch swa_attn_chunk_paged and swa_attn_decode_paged need for these
- * sizes on the current device (its SM count sets how far they split), a
- * multiple of 256; 0 for invalid sizes.
+ * sizes, a multiple of 256; 0 for invalid sizes.  (One run of the work per SM
+ * leaves two partial results at most, so the size depends on d alone.)
  */
 SWA_API size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d);
 SWA_API size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d);

@@ -248,7 +248,7 @@ const char *swa_status_string(int status) {
   }
 }
 
-int swa_version(void) { return (1 << 16) | 0; }
+int swa_version(void) { return (1 << 16) | 1; }
 
 int swa_block_meta(int key_mode, int B, int64_t n_q, int64_t n_k, const int64_t *q_pos0,
                    int64_t W, int tile_q, int tile_k, int8_t *classes, int32_t *ranges,

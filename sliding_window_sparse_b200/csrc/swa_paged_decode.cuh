@@ -273,14 +273,18 @@ __global__ void __launch_bounds__(kPDThreads, 1)
         slot = slot_n;
       }
     }
-    // padded rows: zero, and a log-sum-exp of -infinity
-    for (int b = cta; b < p.B; b += gridDim.x) {
-      if (decode_pos(p, b) >= 0) continue;
-      if (p.pos[b] != -1 && lane == 0) atomicOr(&g_swa_status, SWA_DEV_BADARG);
-      uint4 *o = reinterpret_cast<uint4 *>(p.out + static_cast<int64_t>(b) * p.H * D);
-      for (int i = lane; i < p.H * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
-      if (p.lse)
-        for (int i = lane; i < p.H; i += 32) p.lse[static_cast<int64_t>(b) * p.H + i] = -INFINITY;
+    // padded rows: zero, and a log-sum-exp of -infinity (32 sequences at a look)
+    for (int64_t b0 = static_cast<int64_t>(cta) * 32; b0 < p.B; b0 += gridDim.x * 32) {
+      const int b = static_cast<int>(b0) + lane;
+      const bool pad = b < p.B && decode_pos(p, b) < 0;
+      if (pad && p.pos[b] != -1) atomicOr(&g_swa_status, SWA_DEV_BADARG);
+      for (uint32_t m = __ballot_sync(0xffffffffu, pad); m; m &= m - 1) {
+        const int64_t row = (b0 + __ffs(m) - 1) * p.H;
+        uint4 *o = reinterpret_cast<uint4 *>(p.out + row * D);
+        for (int i = lane; i < p.H * (D / 8); i += 32) o[i] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+          for (int i = lane; i < p.H; i += 32) p.lse[row + i] = -INFINITY;
+      }
     }
     // every copy issued must land before the CTA ends
     if (lane == 0)

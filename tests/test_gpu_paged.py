@@ -547,3 +547,60 @@ def test_serving_run(swa, W, sinks):
     # the first rows see one key: their output is its value, bit for bit
     for b in range(n_seq):
         assert torch.equal(got[cu[b]], v[cu[b]].repeat_interleave(H // Hkv, 0))
+
+
+# ---------------------------------------------------------------------------- at large
+
+def test_many_sequences(swa):
+    """Thousands of sequences, most of them empty or short: a unit list that does not fit the
+    schedule's shared memory, runs that skip long stretches of empty entries."""
+    rng = np.random.default_rng(1)
+    n = 6000
+    lens = rng.choice([0, 1, 2, 40], n, p=[0.5, 0.4, 0.09, 0.01]).tolist()
+    starts = rng.integers(0, 40, n).tolist()
+    b = Batch(lens, starts, 8, 8, 64, 8, 20, 1, seed=2)
+    out, lse = run_chunk(swa, b)
+    assert swa.swa_get_device_status() == 0
+    check_batch(b, out, lse.T)
+    pos = rng.integers(0, 300, 3000).tolist()
+    e = Batch([1] * 3000, pos, 4, 4, 64, 8, 100, 1, seed=3)
+    padded = torch.from_numpy(rng.random(3000) < 0.3).cuda()
+    out, lse = run_decode(swa, e, torch.where(padded, -1, e.t_first))
+    assert swa.swa_get_device_status() == 0
+    want, want_lse, tol, tol_lse = e.expect()
+    keep = (~padded).cpu().numpy()
+    check(to_f64(out)[keep], want[keep], tol[keep], "out")
+    check(to_f64(lse)[keep], want_lse[keep], tol_lse[keep], "lse")
+    assert bool((out[padded] == 0).all()) and bool(torch.isneginf(lse[padded]).all())
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_sweep(swa, seed):
+    """Random batches: group sizes, pages, layouts, windows, sinks, lengths and starts."""
+    rng = np.random.default_rng(1000 + seed)
+
+    def log_int(lo, hi):
+        return int(round(lo * (hi / lo) ** rng.random()))
+
+    Hkv = int(rng.choice([1, 2, 3, 4]))
+    G = int(rng.choice([1, 2, 3, 4, 5, 8, 16, 17, 32]))
+    d = int(rng.choice([64, 128]))
+    page = int(rng.choice([8, 16, 24, 32, 40, 64, 96, 128, 256]))
+    W = log_int(1, 3000) if rng.random() < 0.8 else FULL
+    sinks = int(rng.choice([0, 0, 1, 4, 127, 128]))
+    n = log_int(1, 12)
+    layout = str(rng.choice(["hnd", "nhd"]))
+    if seed % 2:
+        pos = [log_int(1, 9000) - 1 for _ in range(n)]
+        b = Batch([1] * n, pos, G * Hkv, Hkv, d, page, W, sinks, layout, seed=seed)
+        out, lse = run_decode(swa, b)
+    else:
+        lens = [int(rng.choice([0, 1, log_int(1, 300)])) for _ in range(n)]
+        lens[0] = max(1, lens[0])
+        starts = [log_int(1, 4000) - 1 for _ in range(n)]
+        b = Batch(lens, starts, G * Hkv, Hkv, d, page, W, sinks, layout, seed=seed,
+                  lead=int(rng.integers(0, 3)), trail=int(rng.integers(0, 3)))
+        out, lse = run_chunk(swa, b)
+        lse = lse.T
+    assert swa.swa_get_device_status() == 0
+    check_batch(b, out, lse)
