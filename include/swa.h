@@ -563,7 +563,7 @@ SWA_API size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d);
  * or range, a negative start or an end past max_pages * page_size (it is
  * skipped, its rows not written), and for a visible page whose table entry is
  * outside 0 .. n_pages-1 (its keys and values count as zeros).
- * Limits: 1 <= total < 2^31 - 256, n_seq < 2^24, H / Hkv <= 128, d in
+ * Limits: 1 <= total < 2^31 - 256, n_seq * Hkv <= 2^20, H / Hkv <= 128, d in
  * {64, 128}, 0 <= n_sink <= 128, W >= 1 (W past the longest sequence: plain
  * causal attention).
  */

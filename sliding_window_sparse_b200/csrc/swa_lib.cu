@@ -886,6 +886,8 @@ int allow_smem(Kernel kern, int smem, int dev, std::atomic<uint64_t> &done) {
 // Runs that a paged attention call can split into: a bound that does not depend
 // on the device, so that a workspace has one size (148 SMs on a B200).
 constexpr int kPagedRuns = 148;
+// Sequences times key/value heads of a chunk call.
+constexpr int64_t kPagedMaxLists = 1 << 20;
 
 struct DecodePagedWorkspace {
   size_t run, ml, o, bytes;
@@ -1019,7 +1021,10 @@ int swa_paged_append(const void *k_new, int64_t k_new_stride, const void *v_new,
 }
 
 size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d) {
-  return paged_checks(n_seq, total, H, Hkv, d, 1, 0, 1.f) ? 0 : ChunkPagedWorkspace(d).bytes;
+  return paged_checks(n_seq, total, H, Hkv, d, 1, 0, 1.f) ||
+                 static_cast<int64_t>(n_seq) * Hkv > kPagedMaxLists
+             ? 0
+             : ChunkPagedWorkspace(d).bytes;
 }
 
 size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d) {
@@ -1054,6 +1059,9 @@ int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int6
   p.g_inv = ((1 << 16) + p.G - 1) / p.G;
   p.by_hkv = fast_div(Hkv);
   p.by_tu = fast_div(2 * p.tpt);
+  // A CTA walks empty entries of the unit list at about 10^7 a second while the others of
+  // its warps wait, a second at most.
+  if (static_cast<int64_t>(n_seq) * Hkv > kPagedMaxLists) return SWA_ERR_UNSUPPORTED;
   const int64_t slots = (total / (2 * p.tpt) + n_seq) * Hkv;
   if (slots > (1 << 30)) return SWA_ERR_UNSUPPORTED;
   p.n_slots = static_cast<int>(slots);

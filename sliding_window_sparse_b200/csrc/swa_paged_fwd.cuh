@@ -314,6 +314,8 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       hi = c < P ? mul_div(T, c + 1, P) : 0;
     }
   }
+  // the costs above lie where copies of the async proxy write from here on
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

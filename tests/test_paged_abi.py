@@ -133,3 +133,10 @@ def test_workspace_sizes(native):
     assert lib.swa_chunk_paged_workspace_bytes(3, 700, 32, 7, 128) == 0
     assert lib.swa_decode_paged_workspace_bytes(0, 32, 8, 128) == 0
     assert lib.swa_decode_paged_workspace_bytes(3, 32, 8, 96) == 0
+
+
+@pytest.mark.parametrize("n_seq,H,Hkv", [((1 << 20) + 1, 1, 1), ((1 << 17) + 1, 8, 8)])
+def test_chunk_refuses_too_many_sequences(native, n_seq, H, Hkv):
+    assert chunk(native, cache(native), n_seq=n_seq, H=H, Hkv=Hkv) == 2
+    assert native.lib().swa_chunk_paged_workspace_bytes(n_seq, 700, H, Hkv, 128) == 0
+    assert native.lib().swa_chunk_paged_workspace_bytes(n_seq - 1, 700, H, Hkv, 128) > 0
