@@ -956,7 +956,9 @@ int launch_paged_fwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
   if (int e = check_launch_regs(kern, launch_regs)) return e;
   kern<<<grid, swa::kFwd2Threads, L::ALLOC, st>>>(tq, tk, tv, p);
   if (cudaGetLastError() != cudaSuccess) return SWA_ERR_CUDA;
-  return launch_dependent(swa::paged_fwd_merge_kernel<D>, dim3(grid, 2, D / 16), swa::kQT, p, st);
+  return launch_dependent(swa::paged_fwd_merge_kernel<D>,
+                          dim3(grid, 2, D * swa::kQT / (swa::kMergeCols * swa::kMergeThreads)),
+                          swa::kMergeThreads, p, st);
 }
 
 }  // namespace

@@ -13,7 +13,7 @@
 // cut into one run per CTA, so the SMs finish together whatever the lengths
 // are, and a few rows over a long context are spread over all SMs.  A unit
 // that a border cuts leaves unnormalised rows (output, running maximum and
-// sum) that paged_fwd_merge_kernel joins.  Units are listed column by column of
+// sum) that paged_fwd_merge_kernel joins.  Short units are not cut (keep_whole).  Units are listed column by column of
 // a matrix with one column per CTA, so CTAs that run at the same time read
 // neighbouring windows, which L2 holds.
 //
@@ -27,7 +27,7 @@
 //             against 460 us for a prompt of 8192 tokens.)
 //   warp 2    scheduler: walks this CTA's run, 32 list entries at a time, and
 //             hands the units to the other roles through a ring.
-//   warp 3    idle.
+//   warp 3    zeroes the rows outside the sequences on request.
 //   warps 4-7, 8-11   softmax and epilogue of tile A, tile B: a row per thread.
 // Registers, tensor memory and the handshakes of S, P and O are those of
 // fwd2_kernel (swa_fwd2.cuh).
@@ -170,6 +170,25 @@ __device__ __forceinline__ int paged_unit(const PagedFwdParams &p, int u, PagedU
   U.n = (U.qpos + U.ntok - 1) / kKT - first + 1 + (p.n_sink > 0 && first > 0 ? 1 : 0);
   return U.n;
 }
+
+// Whether a unit goes whole to the run in which it starts.  Cutting it balances the runs
+// to a tile, but the parts of 148 cut units cost about 10 us (77 MB of partials written and
+// read back, most of it behind the last tile), some 6 key tiles of an SM.  With units of
+// equal cost the longest run exceeds T / P by the remainder to a whole unit.  Measured, cut
+// against whole, one sequence with 32 own key/value heads (excess in tiles): window 512,
+// 8191 tokens (3) 125 and 117 us, 4096 tokens (5) 72 and 68; window 128, 2047 tokens (2) 34
+// and 28; window 1024, 8191 tokens (5) 163 and 158, 2047 tokens (7) 50 and 51, 4096 tokens
+// (10) 88 and 93.  Long units differ in cost, so that a run may end up far above the mean
+// (window 2048: 235 and 244), and where a run is a tile or two (ten drafted tokens) cutting
+// wins 11 us against 16: few parts are joined in 3 us.
+constexpr int kWholeCost = 12, kWholeExcess = 6, kWholeRun = 3;
+__device__ __forceinline__ bool keep_whole(int64_t T, int P, int most) {
+  if (most > kWholeCost || T < kWholeRun * P || T >= (int64_t(1) << 31) || T == 0) return false;
+  const uint32_t row = static_cast<uint32_t>(P) * most;
+  const uint32_t rounds = (static_cast<uint32_t>(T) + row - 1) / row;
+  return static_cast<int64_t>(rounds) * row - T <= kWholeExcess * P;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kFwd2Threads, 1)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -246,6 +265,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   };
   int64_t T = 0, lo, hi;
   int P = 0;
+  bool whole = false;
   {
     if (blockIdx.x == 0)  // sequences that are skipped
       for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads) {
@@ -254,6 +274,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
           atomicOr(&g_swa_status, SWA_DEV_BADARG);
       }
     int64_t *s_warp = reinterpret_cast<int64_t *>(gbase);
+    int *s_most = reinterpret_cast<int *>(gbase + 256);
     const int per = (n_list + kFwd2Threads - 1) / kFwd2Threads;
     const int s_lo = min(static_cast<int>(threadIdx.x) * per, n_list);
     const int s_hi = min(s_lo + per, n_list);
@@ -264,6 +285,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
     const bool stored = n_list <= static_cast<int>((NK + NV) * L::KV_BYTES / 4);
     const int col0 = s_lo / n_rows, row0 = s_lo - col0 * n_rows;
     int64_t sum = 0, at = 0;
+    int most = 0;  // the largest cost of a unit
     lo = hi = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -280,6 +302,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             const int n = paged_unit(p, row * n_cols + col, U);
             cost = n ? n + kUnitCost : 0;
             if (stored) s_cost[s] = cost;
+            most = max(most, cost);
             if (++row == n_rows) {
               row = 0;
               ++col;
@@ -301,17 +324,23 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
       }
-      if (lane == 31) s_warp[warp] = incl;
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 31) {
+        s_warp[warp] = incl;
+        s_most[warp] = most;
+      }
       __syncthreads();
       at = incl - sum;
       for (int w = 0; w < kFwd2Threads / 32; ++w) {
         if (w < warp) at += s_warp[w];
         T += s_warp[w];
+        most = max(most, s_most[w]);
       }
       const int c = blockIdx.x;
       P = T < n_cols ? static_cast<int>(T) : n_cols;
       lo = c < P ? mul_div(T, c, P) : 0;
       hi = c < P ? mul_div(T, c + 1, P) : 0;
+      whole = keep_whole(T, P, most);
     }
   }
   // the costs above lie where copies of the async proxy write from here on
@@ -605,8 +634,13 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
             if (lane >= o) incl += v;
           }
           const int64_t a = at + incl - cost;  // the unit's tiles are costs [a, a + n)
-          U.t0 = lo - a <= 0 ? 0 : (lo - a < n ? static_cast<int>(lo - a) : n);
-          U.t1 = hi - a <= 0 ? 0 : (hi - a < n ? static_cast<int>(hi - a) : n);
+          if (whole) {  // its start decides
+            U.t0 = 0;
+            U.t1 = a >= lo && a < hi ? n : 0;
+          } else {
+            U.t0 = lo - a <= 0 ? 0 : (lo - a < n ? static_cast<int>(lo - a) : n);
+            U.t1 = hi - a <= 0 ? 0 : (hi - a < n ? static_cast<int>(hi - a) : n);
+          }
           if (n) U.plan(p);
           uint32_t todo = __ballot_sync(0xffffffffu, n && U.t0 < U.t1);
           for (; todo && ok; todo &= todo - 1, ++it) {
@@ -624,6 +658,18 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       }
       PagedUnit none = {};
       if (ok && lane == 0) publish(none);
+    } else if (p.zero_rest) {
+      // ---------------------------------------------------------------- rows outside
+      int64_t a = p.cu_seqlens[0], e = p.cu_seqlens[p.n_seq];
+      a = a < 0 ? 0 : (a > p.total ? p.total : a);
+      e = e < a ? a : (e > p.total ? p.total : e);
+      for (int64_t i = blockIdx.x; i < a + p.total - e; i += gridDim.x) {
+        const int64_t t = i < a ? i : e + i - a;
+        for (int j = lane; j < p.H * (D / 8); j += 32)
+          reinterpret_cast<uint4 *>(p.out + t * p.H * D)[j] = make_uint4(0, 0, 0, 0);
+        if (p.lse)
+          for (int j = lane; j < p.H; j += 32) p.lse[static_cast<int64_t>(j) * p.total + t] = 0;
+      }
     }
   } else {
     warpgroup_regs_inc<kRegsSoftmax>();
@@ -830,31 +876,22 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   }
 }
 
-// Joins the parts of the unit that starts in run blockIdx.x and goes on, one row
-// per thread and 16 columns per CTA: run c's slot 2c + 1, then the slots 2j of
-// the runs that follow.  Also zeroes the rows outside the sequences on request.
+// Joins the parts of the unit that starts in run blockIdx.x and goes on, a row per
+// thread and 8 columns: run c's slot 2c + 1, then the slots 2j of the runs that
+// follow.  Four parts of 8 columns are in flight per thread: two of 16 columns lose 4 us
+// where a unit has ten parts (61 tokens over 130000 keys), four of 16 columns keep half as
+// many threads on an SM and lose 1 to 2 us where units have two.
+constexpr int kMergeThreads = 512;  // 128 rows, 32 columns
+constexpr int kMergeCols = 8;
 template <int D>
-__global__ void __launch_bounds__(kQT) paged_fwd_merge_kernel(const PagedFwdParams p) {
-  if (p.zero_rest) {
-    int64_t a = p.cu_seqlens[0], e = p.cu_seqlens[p.n_seq];
-    a = a < 0 ? 0 : (a > p.total ? p.total : a);
-    e = e < a ? a : (e > p.total ? p.total : e);
-    const int64_t blk = (static_cast<int64_t>(blockIdx.z) * 2 + blockIdx.y) * gridDim.x + blockIdx.x;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * 2 * gridDim.z;
-    for (int64_t i = blk; i < a + p.total - e; i += step) {
-      const int64_t t = i < a ? i : e + i - a;
-      for (int j = threadIdx.x; j < p.H * (D / 8); j += kQT)
-        reinterpret_cast<uint4 *>(p.out + t * p.H * D)[j] = make_uint4(0, 0, 0, 0);
-      if (p.lse)
-        for (int j = threadIdx.x; j < p.H; j += kQT) p.lse[static_cast<int64_t>(j) * p.total + t] = 0;
-    }
-  }
+__global__ void __launch_bounds__(kMergeThreads, 2) paged_fwd_merge_kernel(const PagedFwdParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, x = blockIdx.y, row = threadIdx.x;
+  constexpr int N = kMergeCols / 4, B = 4;  // float4 columns per thread; parts in flight
+  const int c = blockIdx.x, x = blockIdx.y, row = threadIdx.x % kQT;
+  const int col4 = (blockIdx.z * (kMergeThreads / kQT) + threadIdx.x / kQT) * N;
   const int4 run = p.ws_run[c];
   const int rows = min(p.tpt, run.z - x * p.tpt) * p.G;
   if (row >= rows) return;
-  constexpr int N = 4, B = 4;  // float4 columns per thread; parts in flight
   float m = -INFINITY, l = 0.f;
   float4 acc[N];
 #pragma unroll
@@ -869,8 +906,7 @@ __global__ void __launch_bounds__(kQT) paged_fwd_merge_kernel(const PagedFwdPara
         const int64_t slot = (j0 + u == c ? 2 * c + 1 : 2 * (j0 + u)) * 2 + x;
         ml[u] = p.ws_ml[slot * kQT + row];
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-          o[u][i] = p.ws_o[(slot * (D / 4) + blockIdx.z * N + i) * kQT + row];
+        for (int i = 0; i < N; ++i) o[u][i] = p.ws_o[(slot * (D / 4) + col4 + i) * kQT + row];
       }
     }
     float mn = m;
@@ -904,14 +940,14 @@ __global__ void __launch_bounds__(kQT) paged_fwd_merge_kernel(const PagedFwdPara
   const int t = row * p.g_inv >> 16, h = run.y * p.G + row - t * p.G;
   const int64_t tok = run.x + x * p.tpt + t;
   const float inv = 1.f / l;
-  uint4 *dst = reinterpret_cast<uint4 *>(p.out + (tok * p.H + h) * D + blockIdx.z * 4 * N);
+  uint4 *dst = reinterpret_cast<uint4 *>(p.out + (tok * p.H + h) * D + col4 * 4);
 #pragma unroll
   for (int i = 0; i < N; i += 2)
     dst[i / 2] = make_uint4(pack_bf16(acc[i].x * inv, acc[i].y * inv),
                             pack_bf16(acc[i].z * inv, acc[i].w * inv),
                             pack_bf16(acc[i + 1].x * inv, acc[i + 1].y * inv),
                             pack_bf16(acc[i + 1].z * inv, acc[i + 1].w * inv));
-  if (p.lse && blockIdx.z == 0)
+  if (p.lse && col4 == 0)
     p.lse[static_cast<int64_t>(h) * p.total + tok] = (m + __log2f(l)) * 0.6931471805599453f;
 }
 

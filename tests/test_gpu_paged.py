@@ -604,3 +604,26 @@ def test_sweep(swa, seed):
         lse = lse.T
     assert swa.swa_get_device_status() == 0
     check_batch(b, out, lse)
+
+
+SHORT_UNITS = [
+    # lens, starts, H, Hkv, d, page, W, sinks, lead, trail: units of a few key tiles, which the
+    # schedule hands out whole (fewer units than SMs, one and several rounds of them)
+    ([3000], [0], 8, 8, 64, 16, 100, 0, 0, 0),
+    ([3000], [5], 8, 8, 128, 64, 300, 2, 0, 3),
+    ([900, 1, 0, 450, 130], [0, 7, 9, 4000, 255], 24, 24, 64, 32, 129, 0, 2, 40),
+    ([2100], [100], 32, 4, 128, 8, 128, 128, 0, 0),
+    ([1500, 1500], [0, 64], 40, 40, 64, 128, 1, 1, 1, 0),
+]
+
+
+@pytest.mark.parametrize("case", SHORT_UNITS, ids=lambda c: str(c)[:60])
+def test_short_units(swa, case):
+    lens, starts, H, Hkv, d, page, W, sinks, lead, trail = case
+    b = Batch(lens, starts, H, Hkv, d, page, W, sinks, "hnd", seed=H, lead=lead, trail=trail)
+    out, lse = run_chunk(swa, b)
+    assert swa.swa_get_device_status() == 0
+    check_batch(b, out, lse.T, what=str(case)[:40])
+    rest = torch.ones(b.total, dtype=torch.bool)
+    rest[lead:int(b.cu[-1])] = False
+    assert bool((out[rest.cuda()] == 0).all()) and bool((lse.T[rest.cuda()] == 0).all())
