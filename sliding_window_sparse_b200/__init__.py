@@ -26,7 +26,8 @@ import math
 
 import torch
 
-from ._native import PagedCache, Rotation, SwaError, check, lib, status_name  # noqa: F401
+from ._native import (Rotation, SwaError, check, lib, pack_paged_cache,  # noqa: F401
+                      status_name)
 
 __all__ = [
     "SwaError",
@@ -463,7 +464,9 @@ def swa_ring_slot_positions(n_written, W: int, out=None):
 # The paged calls serve single tokens, where the host's time counts: a check asks a tensor once
 # and names it only when it fails, and the stream comes without a Python object around it.
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _bf16 = torch.bfloat16
+_INT_MAX = 0x7FFFFFFF
 
 
 def _elsewhere(index, **named):
@@ -475,7 +478,7 @@ def _elsewhere(index, **named):
 
 def _on(index, call, *args):
     """call(*args, stream) with CUDA device `index` current."""
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         return call(*args, _raw_stream(index))
     with torch.cuda.device(index):
         return call(*args, _raw_stream(index))
@@ -521,15 +524,16 @@ def _paged_cache(k_cache, v_cache, block_table, n_seq):
         raise ValueError("k_cache and v_cache must be bfloat16 CUDA tensors "
                          "[n_pages, Hkv, page_size, d]")
     n_pages, heads, page_size, d = shape
+    page, head, slot, one = strides
     same = v_cache.shape == shape and v_cache.stride() == strides
-    if 1 in shape[:3]:
+    if n_pages == 1 or heads == 1 or page_size == 1:
         # the stride of a dimension of one entry says nothing: any valid one will do
         same = v_cache.shape == shape and all(n == 1 or a == b for n, a, b in
                                               zip(shape, strides, v_cache.stride()))
-        strides = [d if n == 1 else s for n, s in zip(shape[:3], strides)] + [strides[3]]
+        page, head, slot = (d if n == 1 else s for n, s in zip(shape[:3], strides))
     if not same:
         raise ValueError("k_cache and v_cache must have the same shape and strides")
-    if strides[3] != 1:
+    if one != 1:
         raise ValueError("k_cache and v_cache must be contiguous in their last dimension")
     rows = block_table.shape
     if not block_table.is_cuda or block_table.dtype is not torch.int32 or len(rows) != 2 or \
@@ -539,9 +543,9 @@ def _paged_cache(k_cache, v_cache, block_table, n_seq):
     apart, one = block_table.stride()
     if one != 1 and max_pages > 1:
         raise ValueError("block_table must be contiguous along a row")
-    return (PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), strides[0],
-                       strides[1], strides[2], n_pages, max_pages,
-                       apart if n_seq > 1 else max_pages, page_size), heads, d)
+    return (pack_paged_cache(k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), page,
+                             head, slot, n_pages, max_pages, apart if n_seq > 1 else max_pages,
+                             min(page_size, _INT_MAX)), heads, d)
 
 
 def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_start, q=None,
@@ -613,7 +617,7 @@ def swa_paged_append(k_new, v_new, k_cache, v_cache, block_table, cu_seqlens, q_
                    positions=positions, pair_axis=pair_axis)
     check("swa_paged_append",
           _on(index, lib().swa_paged_append, k_new.data_ptr(), ks, v_new.data_ptr(), vs, _ptr(q),
-              qs, _ptr(q_out), qos, ctypes.byref(cache),
+              qs, _ptr(q_out), qos, cache,
               ctypes.byref(rotation) if rotation else None, cu_seqlens.data_ptr(),
               q_start.data_ptr(), n_seq, total, H, Hkv, d, 1 if zero_rest else 0))
     return q_out
@@ -671,7 +675,7 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
         need = swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d)
         workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
     check("swa_attn_chunk_paged",
-          _on(index, lib().swa_attn_chunk_paged, q.data_ptr(), ctypes.byref(cache),
+          _on(index, lib().swa_attn_chunk_paged, q.data_ptr(), cache,
               cu_seqlens.data_ptr(), q_start.data_ptr(), out.data_ptr(), _ptr(lse), n_seq, total,
               H, Hkv, d, W, n_sink, scale, 1 if zero_rest else 0, workspace.data_ptr(),
               workspace.numel() * workspace.element_size()))
@@ -719,7 +723,7 @@ def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
         need = swa_decode_paged_workspace_bytes(B, H, Hkv, d)
         workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
     check("swa_attn_decode_paged",
-          _on(index, lib().swa_attn_decode_paged, q.data_ptr(), ctypes.byref(cache),
+          _on(index, lib().swa_attn_decode_paged, q.data_ptr(), cache,
               pos.data_ptr(), out.data_ptr(), _ptr(lse), B, H, Hkv, d, W, n_sink, scale,
               workspace.data_ptr(), workspace.numel() * workspace.element_size()))
     return (out, lse) if return_lse else out

@@ -140,3 +140,11 @@ def test_chunk_refuses_too_many_sequences(native, n_seq, H, Hkv):
     assert chunk(native, cache(native), n_seq=n_seq, H=H, Hkv=Hkv) == 2
     assert native.lib().swa_chunk_paged_workspace_bytes(n_seq, 700, H, Hkv, 128) == 0
     assert native.lib().swa_chunk_paged_workspace_bytes(n_seq - 1, 700, H, Hkv, 128) > 0
+
+
+def test_packed_cache_is_the_structure(native):
+    fields = (FAKE, FAKE + 256, FAKE + 512, 8192, 1024, 128, 7, 5, 9, 64)
+    packed = native.pack_paged_cache(*fields)
+    assert len(packed) == ctypes.sizeof(native.PagedCache)
+    c = native.PagedCache.from_buffer_copy(packed)
+    assert tuple(getattr(c, name) for name, _ in c._fields_) == fields
