@@ -37,6 +37,17 @@
 // the others an unseen key only reaches scores that the mask replaces; unseen
 // value rows, which a zero weight would not silence (0 * NaN), are zeroed in
 // shared memory by the softmax warps before they hand their weights over.
+//
+// Weights are rounded to bf16 for the second MMA (2^-9 of each on average, the price of
+// its rate); scores, running maximum, sum and output stay in 32 bits.
+//
+// Bound: the chain S -> softmax -> PV of a tile, 1.6 us for both query tiles, where the
+// MMAs and the exponentials of a step (2048 cycles each) would allow 1.1.  Measured with
+// H / Hkv / d = 32 / 8 / 128: a prompt of 8192 tokens 440 us, 1250 TFLOP/s; 4 x 512 tokens
+// over full 4096-key windows 134 us, 1025; 61 tokens over 130000 keys 132 us; five drafted
+// tokens over 1000 keys (8 / 2 / 64) 10.8 us.  Behind the last tile the merge takes 10.6 us
+// where all borders cut a unit and 3 us where none does; a unit's start and epilogue cost
+// about 5 us of its SM.
 #pragma once
 #include <cstdint>
 #include <cuda.h>

@@ -609,11 +609,11 @@ def test_sweep(swa, seed):
 SHORT_UNITS = [
     # lens, starts, H, Hkv, d, page, W, sinks, lead, trail: units of a few key tiles, which the
     # schedule hands out whole (fewer units than SMs, one and several rounds of them)
-    ([3000], [0], 8, 8, 64, 16, 100, 0, 0, 0),
-    ([3000], [5], 8, 8, 128, 64, 300, 2, 0, 3),
-    ([900, 1, 0, 450, 130], [0, 7, 9, 4000, 255], 24, 24, 64, 32, 129, 0, 2, 40),
-    ([2100], [100], 32, 4, 128, 8, 128, 128, 0, 0),
-    ([1500, 1500], [0, 64], 40, 40, 64, 128, 1, 1, 1, 0),
+    ([600], [0], 48, 48, 64, 16, 100, 0, 0, 0),
+    ([700], [5], 40, 40, 128, 64, 300, 2, 0, 3),
+    ([300, 1, 0, 260, 130], [0, 7, 9, 4000, 255], 24, 24, 64, 32, 129, 0, 2, 40),
+    ([400], [100], 128, 16, 128, 8, 128, 128, 0, 0),
+    ([500, 500], [0, 64], 36, 36, 64, 128, 1, 1, 1, 0),
 ]
 
 
