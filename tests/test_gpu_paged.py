@@ -627,3 +627,23 @@ def test_short_units(swa, case):
     rest = torch.ones(b.total, dtype=torch.bool)
     rest[lead:int(b.cu[-1])] = False
     assert bool((out[rest.cuda()] == 0).all()) and bool((lse.T[rest.cuda()] == 0).all())
+
+
+def test_no_tokens(swa):
+    """A step in which every sequence is empty: padding alone, zeros in what the call allocates."""
+    b = Batch([0, 0], [5, 0], 8, 2, 128, 16, 100, 0, trail=70)
+    out, lse = run_chunk(swa, b)
+    assert bool((out == 0).all()) and bool((lse == 0).all())
+    kept, kept_lse = torch.full_like(out, 7.0), torch.full_like(lse, 7.0)
+    run_chunk(swa, b, out=kept, lse=kept_lse)
+    assert bool((kept == 7).all()) and bool((kept_lse == 7).all())
+    before = b.k_cache.clone()
+    k = torch.ones((b.total, 2, 128), dtype=torch.bfloat16, device="cuda")
+    q = swa.swa_paged_append(k, k, b.k_cache, b.v_cache, b.t_table, b.t_cu, b.t_first,
+                             q=b.q.cuda())
+    assert bool((q == 0).all())
+    assert torch.equal(b.k_cache.view(torch.int16), before.view(torch.int16))
+    pos = torch.tensor([-1, -1], device="cuda")
+    out, lse = run_decode(swa, b, pos, q=b.q[:2].cuda())
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    assert swa.swa_get_device_status() == 0
