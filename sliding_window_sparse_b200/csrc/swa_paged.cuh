@@ -20,6 +20,12 @@ struct PagedCache {
   int64_t max_pos = 0;  // positions a table row can map: max_pages * page_size
 };
 
+// Whether positions start .. start + n - 1 (n >= 0) lie in [0, max_pos), for any start:
+// start + n could pass 2^63 and come out negative.
+__host__ __device__ inline bool positions_fit(int64_t start, int64_t n, int64_t max_pos) {
+  return start >= 0 && n <= max_pos && start <= max_pos - n;
+}
+
 // One lane of a converged warp.  Inside a branch on it the compiler knows that a
 // single thread runs, and keeps the operands of MMA and copy instructions in
 // uniform registers; inside a branch on the lane index it does not.
@@ -177,9 +183,10 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Appe
     const int64_t begin = p.cu_seqlens[seq], end = p.cu_seqlens[seq + 1];
     const int64_t start = p.q_start[seq];
     if (begin >= 0 && t >= begin && t < end && end <= p.total) {
-      pos = start + (t - begin);
-      if (start >= 0 && pos < p.c.max_pos)
+      if (positions_fit(start, t - begin + 1, p.c.max_pos)) {
+        pos = start + (t - begin);
         page = p.c.table[seq * p.c.table_stride + pos / p.c.page_size];
+      }
       if (page >= p.c.n_pages) page = -1;
       if (page < 0 && tid == 0) atomicOr(&g_swa_status, SWA_DEV_BADARG);
     }
