@@ -165,7 +165,7 @@ __device__ __forceinline__ int paged_unit(const PagedFwdParams &p, int u, PagedU
       hi = mid;
   }
   const int64_t a = p.cu_seqlens[lo], e = p.cu_seqlens[lo + 1], s = p.q_start[lo];
-  if (a < 0 || e <= a || e > p.total || s < 0 || s + (e - a) > p.c.max_pos) return 0;
+  if (a < 0 || e <= a || e > p.total || !positions_fit(s, e - a, p.c.max_pos)) return 0;
   const uint32_t b0 = p.by_tu(static_cast<uint32_t>(a)) + lo;
   if (q < b0) return 0;
   const uint32_t per = p.by_tu(static_cast<uint32_t>(e)) + lo + 1 - b0;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
     if (blockIdx.x == 0)  // sequences that are skipped
       for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads) {
         const int64_t a = p.cu_seqlens[b], e = p.cu_seqlens[b + 1], s = p.q_start[b];
-        if (a < 0 || e < a || e > p.total || s < 0 || s + (e - a) > p.c.max_pos)
+        if (a < 0 || e < a || e > p.total || !positions_fit(s, e - a, p.c.max_pos))
           atomicOr(&g_swa_status, SWA_DEV_BADARG);
       }
     int64_t *s_warp = reinterpret_cast<int64_t *>(gbase);
