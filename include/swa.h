@@ -552,17 +552,19 @@ SWA_API size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d);
  *      j < n_sink).  All visible positions, the new tokens' own among them,
  *      must be in the cache before the call.
  *   out: [total, H, d] bf16, device;  lse: [H, total] fp32, device, or NULL.
- *   zero_rest: rows of tokens before cu_seqlens[0] and from cu_seqlens[n_seq]
- *      on are left as they were (0), or set to zero in out and lse (1).
+ *   zero_rest: rows that no sequence writes (tokens before cu_seqlens[0] and
+ *      from cu_seqlens[n_seq] on, and those of skipped sequences) are left as
+ *      they were (0), or set to zero in out and lse (1).
  *   workspace: at least swa_chunk_paged_workspace_bytes(...) bytes, 256-byte
  *      aligned, caller-owned, contents on entry ignored; two calls in flight
  *      at once need workspaces of their own.
  * Values of visible slots must be finite; slots that no query of the call may
  * see can hold anything, NaN and infinities included.
- * SWA_ERR_DEVICE is set on the device for a sequence with offsets out of order
- * or range, a negative start or an end past max_pages * page_size (it is
- * skipped, its rows not written), and for a visible page whose table entry is
- * outside 0 .. n_pages-1 (its keys and values count as zeros).
+ * SWA_ERR_DEVICE is set on the device for a sequence with offsets out of
+ * range, a negative start or an end past max_pages * page_size (it is
+ * skipped), for offsets out of order (every sequence is skipped), and for a
+ * visible page whose table entry is outside 0 .. n_pages-1 (its keys and
+ * values count as zeros).
  * Limits: 1 <= total < 2^31 - 256, n_seq * Hkv <= 2^20, H / Hkv <= 128, d in
  * {64, 128}, 0 <= n_sink <= 128, W >= 1 (W past the longest sequence: plain
  * causal attention).

@@ -636,7 +636,8 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
     Query t of sequence b (cu_seqlens int64 [n_seq + 1]) sits at p = q_start[b] + t and reads the
     cached keys j <= p of its own sequence with j >= p - W + 1 or j < n_sink (its own key and
     those of the chunk are in the cache already, see swa_paged_append).  lse is [H, total].  Rows
-    of tokens outside every sequence keep what out and lse held (zeros when allocated here).
+    of tokens outside every sequence, or of a sequence that is skipped because its offsets or
+    start are out of range, keep what out and lse held (zeros when allocated here).
     """
     _need(q, "q", dims=3)
     total, H, d = q.shape
@@ -662,7 +663,7 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
                    cu_seqlens=cu_seqlens, q_start=q_start)
     if not (new_out and lse is None and workspace is None):
         _elsewhere(index, out=out, lse=lse, workspace=workspace)
-    # what is allocated here is zeroed by the call outside the sequences, unless the other of
+    # what is allocated here is zeroed by the call where no sequence writes, unless the other of
     # the two is the caller's: then its rows stay, and ours are zeroed first
     zero_rest = new_out and (new_lse or lse is None)
     if new_out:

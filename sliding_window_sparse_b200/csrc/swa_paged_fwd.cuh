@@ -27,7 +27,8 @@
 //             against 460 us for a prompt of 8192 tokens.)
 //   warp 2    scheduler: walks this CTA's run, 32 list entries at a time, and
 //             hands the units to the other roles through a ring.
-//   warp 3    zeroes the rows outside the sequences on request.
+//   warp 3    zeroes the rows that no unit writes (outside the sequences, or of one that is
+//             skipped), on request.
 //   warps 4-7, 8-11   softmax and epilogue of tile A, tile B: a row per thread.
 // Registers, tensor memory and the handshakes of S, P and O are those of
 // fwd2_kernel (swa_fwd2.cuh).
@@ -147,6 +148,27 @@ struct PagedUnit {
   }
 };
 
+// Whether the call computes a sequence of tokens a .. e - 1 (e >= a) whose first is at
+// position s.
+__device__ __forceinline__ bool takes_sequence(const PagedFwdParams &p, int64_t a, int64_t e,
+                                               int64_t s) {
+  return a >= 0 && e <= p.total && positions_fit(s, e - a, p.c.max_pos);
+}
+
+// Whether a sequence that the call computes holds token t (for offsets in order).
+__device__ __forceinline__ bool writes_token(const PagedFwdParams &p, int64_t t) {
+  if (t < p.cu_seqlens[0] || t >= p.cu_seqlens[p.n_seq]) return false;
+  int lo = 0, hi = p.n_seq;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.cu_seqlens[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return takes_sequence(p, p.cu_seqlens[lo], p.cu_seqlens[lo + 1], p.q_start[lo]);
+}
+
 // Entry u of the unit list: sequence b owns the entries from base(b) * Hkv on, with
 // base(b) = cu[b] / (tokens per unit) + b, which leaves room for its units on every
 // key/value head without a sum over the sequences before it; what is left over
@@ -165,7 +187,7 @@ __device__ __forceinline__ int paged_unit(const PagedFwdParams &p, int u, PagedU
       hi = mid;
   }
   const int64_t a = p.cu_seqlens[lo], e = p.cu_seqlens[lo + 1], s = p.q_start[lo];
-  if (a < 0 || e <= a || e > p.total || !positions_fit(s, e - a, p.c.max_pos)) return 0;
+  if (e <= a || !takes_sequence(p, a, e, s)) return 0;
   const uint32_t b0 = p.by_tu(static_cast<uint32_t>(a)) + lo;
   if (q < b0) return 0;
   const uint32_t per = p.by_tu(static_cast<uint32_t>(e)) + lo + 1 - b0;
@@ -276,14 +298,18 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   };
   int64_t T = 0, lo, hi;
   int P = 0;
-  bool whole = false;
+  bool whole = false, skip_all = false;
   {
-    if (blockIdx.x == 0)  // sequences that are skipped
-      for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads) {
-        const int64_t a = p.cu_seqlens[b], e = p.cu_seqlens[b + 1], s = p.q_start[b];
-        if (a < 0 || e < a || e > p.total || !positions_fit(s, e - a, p.c.max_pos))
-          atomicOr(&g_swa_status, SWA_DEV_BADARG);
-      }
+    // Sequences that are skipped are flagged once.  With offsets out of order the list below
+    // would lose some sequences and tokens could be in several: every CTA sees it, and has no
+    // unit then.
+    int unordered = 0;
+    for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads) {
+      const int64_t a = p.cu_seqlens[b], e = p.cu_seqlens[b + 1];
+      unordered |= e < a;
+      if (blockIdx.x == 0 && (e < a || !takes_sequence(p, a, e, p.q_start[b])))
+        atomicOr(&g_swa_status, SWA_DEV_BADARG);
+    }
     int64_t *s_warp = reinterpret_cast<int64_t *>(gbase);
     int *s_most = reinterpret_cast<int *>(gbase + 256);
     const int per = (n_list + kFwd2Threads - 1) / kFwd2Threads;
@@ -340,13 +366,14 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         s_warp[warp] = incl;
         s_most[warp] = most;
       }
-      __syncthreads();
+      skip_all = __syncthreads_or(unordered);
       at = incl - sum;
       for (int w = 0; w < kFwd2Threads / 32; ++w) {
         if (w < warp) at += s_warp[w];
         T += s_warp[w];
         most = max(most, s_most[w]);
       }
+      if (skip_all) T = 0;
       const int c = blockIdx.x;
       P = T < n_cols ? static_cast<int>(T) : n_cols;
       lo = c < P ? mul_div(T, c, P) : 0;
@@ -671,15 +698,19 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       if (ok && lane == 0) publish(none);
     } else if (p.zero_rest) {
       // ---------------------------------------------------------------- rows outside
-      int64_t a = p.cu_seqlens[0], e = p.cu_seqlens[p.n_seq];
-      a = a < 0 ? 0 : (a > p.total ? p.total : a);
-      e = e < a ? a : (e > p.total ? p.total : e);
-      for (int64_t i = blockIdx.x; i < a + p.total - e; i += gridDim.x) {
-        const int64_t t = i < a ? i : e + i - a;
-        for (int j = lane; j < p.H * (D / 8); j += 32)
-          reinterpret_cast<uint4 *>(p.out + t * p.H * D)[j] = make_uint4(0, 0, 0, 0);
-        if (p.lse)
-          for (int j = lane; j < p.H; j += 32) p.lse[static_cast<int64_t>(j) * p.total + t] = 0;
+      // Tokens of padding and of skipped sequences: 32 are looked up at once, one per lane, a
+      // grid apart, so that a stretch of them is spread over all CTAs.
+      const int64_t apart = gridDim.x;
+      for (int64_t t0 = blockIdx.x; t0 < p.total; t0 += 32 * apart) {
+        const int64_t mine = t0 + lane * apart;
+        const bool rest = mine < p.total && (skip_all || !writes_token(p, mine));
+        for (uint32_t m = __ballot_sync(0xffffffffu, rest); m; m &= m - 1) {
+          const int64_t t = t0 + (__ffs(m) - 1) * apart;
+          for (int j = lane; j < p.H * (D / 8); j += 32)
+            reinterpret_cast<uint4 *>(p.out + t * p.H * D)[j] = make_uint4(0, 0, 0, 0);
+          if (p.lse)
+            for (int j = lane; j < p.H; j += 32) p.lse[static_cast<int64_t>(j) * p.total + t] = 0;
+        }
       }
     }
   } else {

@@ -53,3 +53,56 @@ def test_chunk_refuses_starts_at_the_ends_of_64_bits(swa, start, which):
         else:
             check(to_f64(out[rows]), want[rows], tol[rows], "out")
             check(to_f64(lse[:, rows].T), want_lse[rows], tol_lse[rows], "lse")
+
+
+def nan_memory(*shapes):
+    """Leaves NaN in the blocks that the next tensors of these shapes get."""
+    held = [torch.full(shape, float("nan"), dtype=dtype, device="cuda") for shape, dtype in shapes]
+    torch.cuda.synchronize()
+    del held
+
+
+@pytest.mark.parametrize("cu,first,skipped", [
+    ([0, 20, 50, 60], [5, -1, 0], [(20, 50)]),                    # a negative start
+    ([0, 20, 50, 60], [1 << 62, 100, 0], [(0, 20)]),              # an end past the table
+    ([0, 20, 50, 61], [5, 100, 0], [(50, 60)]),                   # offsets past the tokens
+    ([-4, 20, 50, 60], [5, 100, 0], [(0, 20)]),                   # offsets before them
+    ([3, 20, 50, 56], [5, -7, 0], [(0, 3), (20, 50), (56, 60)]),  # and padding on either side
+    ([0, 20, 50, 60], [-1, -1, -1], [(0, 60)]),
+    ([0, 60, 60, 60], [-1, 100, 0], [(0, 60)]),
+])
+def test_chunk_rows_of_skipped_sequences_are_zero(swa, cu, first, skipped):
+    """In tensors that the call allocates every row that no sequence writes is zero."""
+    b = Batch([20, 30, 10], [5, 100, 0], 4, 2, 64, 16, 64, 0)
+    t_cu = torch.tensor(cu, dtype=torch.int64, device="cuda")
+    t_first = torch.tensor(first, dtype=torch.int64, device="cuda")
+    q = b.q.cuda()
+    nan_memory(((60, 4, 64), torch.bfloat16), ((4, 60), torch.float32))
+    out, lse = swa.swa_attn_chunk_paged(q, b.k_cache, b.v_cache, b.t_table, t_cu, t_first, b.W,
+                                        b.scale, return_lse=True)
+    assert swa.swa_get_device_status() == 6
+    zero = torch.zeros(60, dtype=torch.bool)
+    for lo, hi in skipped:
+        zero[lo:hi] = True
+    zero = zero.cuda()
+    assert bool((out[zero] == 0).all()) and bool((lse[:, zero] == 0).all())
+    written = out[~zero].float().abs().amax(-1)  # a row of d values is not all zero by chance
+    assert bool((written > 0).all()) and bool(torch.isfinite(lse[:, ~zero]).all())
+
+
+@pytest.mark.parametrize("cu", [[0, 20, 10, 60], [50, 0, 60, 60], [10, 40, 20, 30], [60, 0, 0, 60],
+                                [0, 60, 59, 60], [0, 5, (1 << 63) - 1, -1]])
+def test_chunk_skips_all_under_disordered_offsets(swa, cu):
+    """Offsets out of order: flagged, rows of new tensors are zero, the caller's are left."""
+    b = Batch([20, 30, 10], [5, 100, 0], 4, 2, 64, 16, 64, 0)
+    t_cu = torch.tensor(cu, device="cuda")
+    args = (b.q.cuda(), b.k_cache, b.v_cache, b.t_table, t_cu, b.t_first, b.W, b.scale)
+    nan_memory(((60, 4, 64), torch.bfloat16), ((4, 60), torch.float32))
+    out, lse = swa.swa_attn_chunk_paged(*args, return_lse=True)
+    assert swa.swa_get_device_status() == 6
+    assert bool((out == 0).all()) and bool((lse == 0).all())
+    out.fill_(7)
+    lse.fill_(7)
+    swa.swa_attn_chunk_paged(*args, out=out, lse=lse)
+    assert swa.swa_get_device_status() == 6
+    assert bool((out == 7).all()) and bool((lse == 7).all())
