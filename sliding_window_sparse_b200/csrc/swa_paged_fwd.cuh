@@ -248,6 +248,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   const uint32_t BAR_UE = BAR_UF + 8 * kUnitRing;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(gbase + L::OFF_MISC);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(gbase + L::OFF_MISC + 4);
+  volatile int *skip_all = reinterpret_cast<volatile int *>(gbase + L::OFF_MISC + 24);
   int64_t *s_run = reinterpret_cast<int64_t *>(gbase + L::OFF_MISC + 8);  // entry, its offset
   int4 *s_unit = reinterpret_cast<int4 *>(gbase + L::OFF_UNIT);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       mbar_init(BAR_UE + 8 * s, 10);  // producer, MMA thread, eight softmax warps
     }
     *abort_flag = 0;
+    *skip_all = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -298,18 +300,14 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
   };
   int64_t T = 0, lo, hi;
   int P = 0;
-  bool whole = false, skip_all = false;
+  bool whole = false;
   {
-    // Sequences that are skipped are flagged once.  With offsets out of order the list below
-    // would lose some sequences and tokens could be in several: every CTA sees it, and has no
-    // unit then.
-    int unordered = 0;
-    for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads) {
-      const int64_t a = p.cu_seqlens[b], e = p.cu_seqlens[b + 1];
-      unordered |= e < a;
-      if (blockIdx.x == 0 && (e < a || !takes_sequence(p, a, e, p.q_start[b])))
-        atomicOr(&g_swa_status, SWA_DEV_BADARG);
-    }
+    if (blockIdx.x == 0)  // sequences that are skipped
+      for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads) {
+        const int64_t a = p.cu_seqlens[b], e = p.cu_seqlens[b + 1];
+        if (e < a || !takes_sequence(p, a, e, p.q_start[b]))
+          atomicOr(&g_swa_status, SWA_DEV_BADARG);
+      }
     int64_t *s_warp = reinterpret_cast<int64_t *>(gbase);
     int *s_most = reinterpret_cast<int *>(gbase + 256);
     const int per = (n_list + kFwd2Threads - 1) / kFwd2Threads;
@@ -366,14 +364,13 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         s_warp[warp] = incl;
         s_most[warp] = most;
       }
-      skip_all = __syncthreads_or(unordered);
+      __syncthreads();
       at = incl - sum;
       for (int w = 0; w < kFwd2Threads / 32; ++w) {
         if (w < warp) at += s_warp[w];
         T += s_warp[w];
         most = max(most, s_most[w]);
       }
-      if (skip_all) T = 0;
       const int c = blockIdx.x;
       P = T < n_cols ? static_cast<int>(T) : n_cols;
       lo = c < P ? mul_div(T, c, P) : 0;
@@ -381,6 +378,10 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       whole = keep_whole(T, P, most);
     }
   }
+  // With offsets out of order the list loses some sequences and tokens can be in several: every
+  // CTA sees it, and has no unit then.
+  for (int b = threadIdx.x; b < p.n_seq; b += kFwd2Threads)
+    if (p.cu_seqlens[b + 1] < p.cu_seqlens[b]) *skip_all = 1;
   // the costs above lie where copies of the async proxy write from here on
   fence_async_smem();
   tc_fence_before();
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
         mbar_arrive(BAR_UF + 8 * r);
         return true;
       };
-      if (hi > lo) {
+      if (hi > lo && !*skip_all) {
         int s = static_cast<int>(s_run[0]);
         int64_t at = s_run[1];
         while (ok && at < hi && s < n_list) {
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(kFwd2Threads, 1)
       const int64_t apart = gridDim.x;
       for (int64_t t0 = blockIdx.x; t0 < p.total; t0 += 32 * apart) {
         const int64_t mine = t0 + lane * apart;
-        const bool rest = mine < p.total && (skip_all || !writes_token(p, mine));
+        const bool rest = mine < p.total && (*skip_all || !writes_token(p, mine));
         for (uint32_t m = __ballot_sync(0xffffffffu, rest); m; m &= m - 1) {
           const int64_t t = t0 + (__ffs(m) - 1) * apart;
           for (int j = lane; j < p.H * (D / 8); j += 32)
