@@ -562,9 +562,10 @@ SWA_API size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d);
  * see can hold anything, NaN and infinities included.
  * SWA_ERR_DEVICE is set on the device for a sequence with offsets out of
  * range, a negative start or an end past max_pages * page_size (it is
- * skipped), for offsets out of order (every sequence is skipped), and for a
- * visible page whose table entry is outside 0 .. n_pages-1 (its keys and
- * values count as zeros).
+ * skipped; the start of a sequence without tokens is not looked at), for
+ * offsets out of order (every sequence is skipped), and for a visible page
+ * whose table entry is outside 0 .. n_pages-1 (its keys and values count as
+ * zeros).
  * Limits: 1 <= total < 2^31 - 256, n_seq * Hkv <= 2^20, H / Hkv <= 128, d in
  * {64, 128}, 0 <= n_sink <= 128, W >= 1 (W past the longest sequence: plain
  * causal attention).

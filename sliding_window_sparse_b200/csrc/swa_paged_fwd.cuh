@@ -148,11 +148,11 @@ struct PagedUnit {
   }
 };
 
-// Whether the call computes a sequence of tokens a .. e - 1 (e >= a) whose first is at
-// position s.
+// Whether tokens a .. e - 1 (e >= a), the first at position s, are a sequence that the call can
+// compute.  An empty one may have any start: batches are padded with them.
 __device__ __forceinline__ bool takes_sequence(const PagedFwdParams &p, int64_t a, int64_t e,
                                                int64_t s) {
-  return a >= 0 && e <= p.total && positions_fit(s, e - a, p.c.max_pos);
+  return a >= 0 && e <= p.total && (e == a || positions_fit(s, e - a, p.c.max_pos));
 }
 
 // Whether a sequence that the call computes holds token t (for offsets in order).

@@ -8,7 +8,7 @@ import torch
 
 from tests._paged import Batch
 from tests._util import to_f64
-from tests.test_gpu_paged import check, fused, swa  # noqa: F401
+from tests.test_gpu_paged import check, check_batch, fused, swa  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,23 @@ def test_chunk_skips_all_under_disordered_offsets(swa, cu):
     swa.swa_attn_chunk_paged(*args, out=out, lse=lse)
     assert swa.swa_get_device_status() == 6
     assert bool((out == 7).all()) and bool((lse == 7).all())
+
+
+@pytest.mark.parametrize("start", [-1, 1 << 20, (1 << 63) - 1])
+def test_empty_sequences_may_have_any_start(swa, start):
+    """A batch of fixed size padded with empty sequences: no flag, by append or by attention."""
+    b = Batch([3, 0, 40, 0], [7, 0, 130, 0], 4, 2, 64, 16, 50, 2)
+    first = b.t_first.clone()
+    first[1] = first[3] = start
+    out, lse = swa.swa_attn_chunk_paged(b.q.cuda(), b.k_cache, b.v_cache, b.t_table, b.t_cu, first,
+                                        b.W, b.scale, n_sink=2, return_lse=True)
+    assert swa.swa_get_device_status() == 0
+    check_batch(b, out, lse.T)
+    k = torch.randn((43, 2, 64), device="cuda").bfloat16()
+    swa.swa_paged_append(k, k, b.k_cache, b.v_cache, b.t_table, b.t_cu, first)
+    assert swa.swa_get_device_status() == 0
+    none = torch.zeros_like(b.t_cu)
+    out = swa.swa_attn_chunk_paged(b.q.cuda(), b.k_cache, b.v_cache, b.t_table, none,
+                                   torch.full_like(first, start), b.W, b.scale)
+    assert swa.swa_get_device_status() == 0
+    assert bool((out == 0).all())
