@@ -462,9 +462,10 @@ def swa_ring_slot_positions(n_written, W: int, out=None):
 
 
 # The paged calls serve single tokens, where the host's time counts: a check asks a tensor once
-# and names it only when it fails, and the stream comes without a Python object around it.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# and names it only when it fails, and the stream comes without a Python object around it.  (Torch
+# keeps these two to itself, and a build without CUDA has neither: the public calls stand in.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _bf16 = torch.bfloat16
 _INT_MAX = 0x7FFFFFFF
 
