@@ -484,7 +484,8 @@ __global__ void __launch_bounds__(kPDThreads, 1)
 #pragma unroll
         for (int w = 0; w < kPDWarps; ++w) {
           const float2 ml = s_ml[w * 16 + row];
-          Ls += ml.x == -INFINITY ? 0.f : ml.y * ex2(ml.x - M);
+          // without a finite score the sum is 0, or NaN and stays so
+          Ls += ml.y * (ml.x == -INFINITY ? 0.f : ex2(ml.x - M));
           const float4 v =
               *reinterpret_cast<const float4 *>(s_red + (w * halves * 8 + row) * cols + col);
           a.x += v.x;
@@ -543,13 +544,15 @@ __global__ void __launch_bounds__(128) paged_decode_merge_kernel(const PagedDeco
       }
       float mn = M;
 #pragma unroll
-      for (int k = 0; k < N; ++k) mn = fmaxf(mn, ml[k].x);  // part c has a key: finite
-      const float w0 = ex2(M - mn);
+      for (int k = 0; k < N; ++k) mn = fmaxf(mn, ml[k].x);
+      // A maximum of -infinity (all scores of the parts are that, or NaN) gives weight 0, which
+      // leaves sums of 0 as they are, and NaN.
+      const float w0 = M == -INFINITY ? 0.f : ex2(M - mn);
       Ls *= w0;
       a = make_float4(a.x * w0, a.y * w0, a.z * w0, a.w * w0);
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const float w = ex2(ml[k].x - mn);
+        const float w = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - mn);
         Ls = fmaf(ml[k].y, w, Ls);
         a.x = fmaf(v[k].x, w, a.x);
         a.y = fmaf(v[k].y, w, a.y);

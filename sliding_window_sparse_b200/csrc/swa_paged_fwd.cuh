@@ -955,7 +955,7 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_fwd_merge_kernel(const
     float mn = m;
 #pragma unroll
     for (int u = 0; u < B; ++u)
-      if (ml[u].y > 0.f) mn = fmaxf(mn, ml[u].x);
+      if (ml[u].y != 0.f) mn = fmaxf(mn, ml[u].x);
     const float w0 = m == -INFINITY ? 0.f : ex2(m - mn);
     l *= w0;
 #pragma unroll
@@ -967,7 +967,8 @@ __global__ void __launch_bounds__(kMergeThreads, 2) paged_fwd_merge_kernel(const
     }
 #pragma unroll
     for (int u = 0; u < B; ++u) {
-      if (!(ml[u].y > 0.f)) continue;  // the part gave this row no key: its O is not written
+      // the part gave this row no key: its O may not be written (a sum that is NaN stays in)
+      if (ml[u].y == 0.f) continue;
       const float w = ex2(ml[u].x - mn);
       l = fmaf(ml[u].y, w, l);
 #pragma unroll

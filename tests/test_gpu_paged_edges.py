@@ -8,7 +8,8 @@ import torch
 
 from tests._paged import Batch
 from tests._util import to_f64
-from tests.test_gpu_paged import check, check_batch, fused, swa  # noqa: F401
+from tests.test_gpu_paged import (FULL, check, check_batch, fused, run_chunk, run_decode,  # noqa: F401
+                                  swa)
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +127,82 @@ def test_empty_sequences_may_have_any_start(swa, start):
                                    torch.full_like(first, start), b.W, b.scale)
     assert swa.swa_get_device_status() == 0
     assert bool((out == 0).all())
+
+
+def not_finite(b, q, k):
+    """[tokens, H] rows whose softmax has a NaN or +infinity among its seen scores; q [tokens, H, d]
+    and the one sequence's keys k [positions, Hkv, d] in 64 bits."""
+    n, H, d = q.shape
+    with np.errstate(invalid="ignore", over="ignore"):
+        x = np.einsum("thgd,khd->thgk", q.reshape(n, b.Hkv, H // b.Hkv, d), k)
+    qp = b.starts[0] + np.arange(n)
+    seen = (b.pos_of[0] <= qp[:, None]) & (b.pos_of[0] > qp[:, None] - b.W)
+    return ((np.isnan(x) | np.isposinf(x)) & seen[:, None, None]).any(-1).reshape(n, H)
+
+
+@pytest.mark.parametrize("what", ["key", "query"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("at", [10, 700, 15000, 30010])
+def test_a_nan_is_not_lost_between_parts(swa, what, value, at):
+    """Few rows over many keys, so the work of a row is cut into parts: a NaN or infinite score in
+    any of them makes the row and its log-sum-exp NaN, and no other row."""
+    b = Batch([17], [30000], 8, 2, 128, 16, FULL, 0)
+    q = b.q.cuda()
+    page, slot = int(b.table[0, at // 16]), at % 16
+    if what == "key":
+        b.k_cache[page, 1, slot, 5] = value
+        b.keys[0][at, 1, 5] = value
+    else:
+        q[at % 17, at % 8, 5] = value
+    bad = not_finite(b, to_f64(q), b.keys[0].double().numpy())
+    assert bad.any() and not bad.all()
+    out, lse = swa.swa_attn_chunk_paged(q, b.k_cache, b.v_cache, b.t_table, b.t_cu, b.t_first, b.W,
+                                        b.scale, return_lse=True)
+    assert np.array_equal(np.isnan(to_f64(lse.T)), bad)
+    assert np.array_equal(np.isnan(to_f64(out)).any(-1), bad)
+    assert np.array_equal(np.isnan(to_f64(out)).all(-1), bad)
+    # the last token alone
+    out, lse = swa.swa_attn_decode_paged(q[-1:], b.k_cache, b.v_cache, b.t_table, b.t_first + 16,
+                                         b.W, b.scale, return_lse=True)
+    bad = bad[-1:]
+    assert np.array_equal(np.isnan(to_f64(lse)), bad)
+    assert np.array_equal(np.isnan(to_f64(out)).any(-1), bad)
+    assert np.array_equal(np.isnan(to_f64(out)).all(-1), bad)
+
+
+def test_a_nan_query_in_one_part(swa):
+    """A row whose work is one part, or one warp's keys: output and log-sum-exp are NaN."""
+    b = Batch([1] * 4, [0, 3, 200, 17], 8, 2, 64, 16, FULL, 0)
+    q = b.q.cuda()
+    q[1, 2, 0] = q[2, 7, 63] = q[0, 0, 9] = float("nan")
+    for out, lse in (swa.swa_attn_decode_paged(q, b.k_cache, b.v_cache, b.t_table, b.t_first, b.W,
+                                               b.scale, return_lse=True),
+                     swa.swa_attn_chunk_paged(q, b.k_cache, b.v_cache, b.t_table, b.t_cu,
+                                              b.t_first, b.W, b.scale, return_lse=True)):
+        if lse.shape != (4, 8):
+            lse = lse.T
+        bad = torch.isnan(q).any(-1)
+        assert torch.equal(torch.isnan(lse), bad)
+        assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(
+            torch.isnan(out).any(-1), bad)
+
+
+@pytest.mark.parametrize("first_seen", [130, 1300, 20000])
+def test_keys_of_the_lowest_value(swa, first_seen):
+    """The keys before first_seen hold the type's lowest value in one dimension, so that their scores
+    are -infinity in 32 bits and their weights zero: the rows are those of the keys behind them."""
+    n = first_seen + 300
+    b = Batch([1], [n - 1], 8, 2, 64, 16, FULL, 0)
+    b.q[:, :, 0] = 4.0
+    lowest = torch.finfo(torch.bfloat16).min
+    at = torch.from_numpy(b.table[0, np.arange(first_seen) // 16].astype(np.int64)).cuda()
+    slot = torch.from_numpy(np.arange(first_seen) % 16).cuda()
+    b.k_cache[at, :, slot, 0] = lowest
+    # the definition on the keys behind: a window of the 300 last positions
+    near = Batch([1], [n - 1], 8, 2, 64, 16, 300, 0)
+    near.q, near.pos_of = b.q, [np.arange(first_seen, n)]
+    near.keys, near.vals = [b.keys[0][first_seen:]], [b.vals[0][first_seen:]]
+    for run in (run_decode, run_chunk):
+        out, lse = run(swa, b)
+        check_batch(near, out, lse.T if run is run_chunk else lse)
+    assert swa.swa_get_device_status() == 0
