@@ -20,6 +20,11 @@
 // in the registers of the warp that needs them.  Query heads beyond G fill the
 // 16 rows with zeros.
 //
+// P goes in as two terms of 16 bits, the second one the rounding of the first,
+// so a weight loses 2^-16 where one term would lose 2^-8.  Up to 8 query heads
+// leave rows 8-15 free: the second terms fill them, and the two halves of O are
+// added in the end.  More heads take a second MMA per fragment (384 a tile).
+//
 // Measured (H / Hkv / d = 32 / 8 / 128): 64 sequences of 4096-key windows in pages of
 // 16 slots 172 us, 6.3 TB/s (a copy reaches 6.56); 24 sequences of up to 100000 keys with
 // 64 query heads in pages of 64 slots 773 us, 7.0 TB/s; one sequence of 1000 keys 8.6 us,
@@ -322,6 +327,7 @@ __global__ void __launch_bounds__(kPDThreads, 1)
     bool ok = true;
     const int kvh = r.kh / p.HB, hb = r.kh % p.HB;
     const int rows = min(kPDRows, p.G - hb * kPDRows);
+    const bool few = rows <= 8;  // rows 8-15 of P: the second terms of rows 0-7
     const int64_t h0 = static_cast<int64_t>(r.b) * p.H + kvh * p.G + hb * kPDRows;
     uint32_t qa[D / 16][4];
     {
@@ -397,43 +403,65 @@ __global__ void __launch_bounds__(kPDThreads, 1)
           grow |= g;
         }
         if (__any_sync(0xffffffffu, grow)) {
+          l[0] *= al[0];
+          l[1] *= al[1];
+          if (few) al[1] = al[0];
 #pragma unroll
           for (int n = 0; n < D / 8; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[n][e] *= al[e >> 1];
-          l[0] *= al[0];
-          l[1] *= al[1];
         }
-        uint32_t pa[4];  // P as the A operand: rows gr / gr + 8, keys of either half
+        // P as the A operand (rows gr / gr + 8, keys of either half) and its rounding
+        uint32_t pa[4], pb[4];
+        auto weigh = [&](int x) {
+          const float mu = m[x] == -INFINITY ? 0.f : m[x];
 #pragma unroll
-        for (int nb = 0; nb < 2; ++nb)
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float mu = m[x] == -INFINITY ? 0.f : m[x];
+          for (int nb = 0; nb < 2; ++nb) {
             const float w0 = ex2(fmaf(s[nb][2 * x], p.scale_log2, -mu));
             const float w1 = ex2(fmaf(s[nb][2 * x + 1], p.scale_log2, -mu));
             l[x] += w0 + w1;
-            pa[nb * 2 + x] = pack_bf16(w0, w1);
+            const uint32_t hi = pack_bf16(w0, w1);
+            pa[nb * 2 + x] = hi;
+            pb[nb * 2 + x] = pack_bf16(w0 - __uint_as_float(hi << 16),
+                                       w1 - __uint_as_float(hi & 0xFFFF0000u));
           }
-#pragma unroll
-        for (int n2 = 0; n2 < D / 16; ++n2) {
-          uint32_t vb[4];
-          const uint32_t c = (n2 & 3) * 2 + v_half;
-          ldsm4t(vb, stage + (n2 >> 2) * panel + v_off + ((c ^ sw_v) << 4));
-          if (!whole) {
-            vb[0] &= keep[0];
-            vb[1] &= keep[1];
-            vb[2] &= keep[0];
-            vb[3] &= keep[1];
-          }
-          mma16816(o[2 * n2], pa, vb[0], vb[1]);
-          mma16816(o[2 * n2 + 1], pa, vb[2], vb[3]);
+        };
+        weigh(0);
+        if (few) {
+          pa[1] = pb[0];
+          pa[3] = pb[2];
+        } else {
+          weigh(1);
         }
+        auto add_pv = [&](const uint32_t(&pw)[4]) {
+#pragma unroll
+          for (int n2 = 0; n2 < D / 16; ++n2) {
+            uint32_t vb[4];
+            const uint32_t c = (n2 & 3) * 2 + v_half;
+            ldsm4t(vb, stage + (n2 >> 2) * panel + v_off + ((c ^ sw_v) << 4));
+            if (!whole) {
+              vb[0] &= keep[0];
+              vb[1] &= keep[1];
+              vb[2] &= keep[0];
+              vb[3] &= keep[1];
+            }
+            mma16816(o[2 * n2], pw, vb[0], vb[1]);
+            mma16816(o[2 * n2 + 1], pw, vb[2], vb[3]);
+          }
+        };
+        add_pv(pa);
+        if (!few) add_pv(pb);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(BAR_E + 8 * st);
     }
 
+    if (few)
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] += o[n][2];
+        o[n][1] += o[n][3];
+      }
     // Join the eight warps' states: a common maximum per row, then sums through shared
     // memory, 8 rows x D or 16 rows x 64 columns at a time.
 #pragma unroll

@@ -206,3 +206,21 @@ def test_keys_of_the_lowest_value(swa, first_seen):
         out, lse = run(swa, b)
         check_batch(near, out, lse.T if run is run_chunk else lse)
     assert swa.swa_get_device_status() == 0
+
+
+@pytest.mark.parametrize("pos,H,Hkv,d,page", [
+    ([1, 2, 4, 7, 12, 15, 30, 61], 32, 8, 64, 16),
+    ([3, 9, 33, 100], 40, 2, 128, 32),
+])
+def test_decode_weights_keep_32_bits(swa, pos, H, Hkv, d, page):
+    """The weights reach the second product with an error of 2^-16, as two terms of 16 bits: each
+    term is rounded by at most 2^-8 of what it stands for, the second stands for the first one's
+    rounding.  (With one term the weights are off by up to 2^-8.)"""
+    b = Batch([1] * len(pos), pos, H, Hkv, d, page, FULL, 0, seed=11)
+    out, lse = run_decode(swa, b)
+    want, want_lse, tol, tol_lse = b.expect()
+    b.vals = [v.abs() for v in b.vals]
+    mean_abs = b.expect()[0]  # the weighted mean of |v|
+    tol -= (2.0 ** -8 - 2.0 ** -16) * mean_abs * (1 + 2.0 ** -8)
+    check(to_f64(out), want, tol, "out")
+    check(to_f64(lse), want_lse, tol_lse, "lse")
