@@ -534,7 +534,7 @@ SWA_API int swa_paged_append(const void *k_new, int64_t k_new_stride, const void
 /*
  * swa_chunk_paged_workspace_bytes, swa_decode_paged_workspace_bytes -- bytes
  * of scratch swa_attn_chunk_paged and swa_attn_decode_paged need for these
- * sizes, a multiple of 256; 0 for invalid sizes.  (One run of the work per SM
+ * sizes, a multiple of 256; 0 for sizes that the call refuses.  (One run of the work per SM
  * leaves two partial results at most, so the size depends on d alone.)
  */
 SWA_API size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d);

@@ -886,8 +886,28 @@ int allow_smem(Kernel kern, int smem, int dev, std::atomic<uint64_t> &done) {
 // Runs that a paged attention call can split into: a bound that does not depend
 // on the device, so that a workspace has one size (148 SMs on a B200).
 constexpr int kPagedRuns = 148;
-// Sequences times key/value heads of a chunk call.
+// Sequences times key/value heads of a chunk call: a CTA walks empty entries of the unit list at
+// about 10^7 a second while the others of its warps wait, a second at most.
 constexpr int64_t kPagedMaxLists = 1 << 20;
+
+// Entries of a chunk call's unit list.
+int64_t unit_slots(int n_seq, int64_t total, int H, int Hkv) {
+  return (total / (2 * (kBQ / (H / Hkv))) + n_seq) * Hkv;
+}
+
+int chunk_paged_checks(int n_seq, int64_t total, int H, int Hkv, int d, int64_t W, int n_sink,
+                       float scale) {
+  if (int e = paged_checks(n_seq, total, H, Hkv, d, W, n_sink, scale)) return e;
+  if (H / Hkv > 128 || static_cast<int64_t>(n_seq) * Hkv > kPagedMaxLists ||
+      unit_slots(n_seq, total, H, Hkv) > (1 << 30))
+    return SWA_ERR_UNSUPPORTED;
+  return SWA_OK;
+}
+
+int decode_paged_checks(int B, int H, int Hkv, int d, int64_t W, int n_sink, float scale) {
+  if (int e = paged_checks(B, B, H, Hkv, d, W, n_sink, scale)) return e;
+  return static_cast<int64_t>(B) * H > (1 << 24) ? SWA_ERR_UNSUPPORTED : SWA_OK;
+}
 
 struct DecodePagedWorkspace {
   size_t run, ml, o, bytes;
@@ -1023,25 +1043,21 @@ int swa_paged_append(const void *k_new, int64_t k_new_stride, const void *v_new,
 }
 
 size_t swa_chunk_paged_workspace_bytes(int n_seq, int64_t total, int H, int Hkv, int d) {
-  return paged_checks(n_seq, total, H, Hkv, d, 1, 0, 1.f) ||
-                 static_cast<int64_t>(n_seq) * Hkv > kPagedMaxLists
-             ? 0
-             : ChunkPagedWorkspace(d).bytes;
+  return chunk_paged_checks(n_seq, total, H, Hkv, d, 1, 0, 1.f) ? 0 : ChunkPagedWorkspace(d).bytes;
 }
 
 size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d) {
-  return paged_checks(B, B, H, Hkv, d, 1, 0, 1.f) ? 0 : DecodePagedWorkspace(d).bytes;
+  return decode_paged_checks(B, H, Hkv, d, 1, 0, 1.f) ? 0 : DecodePagedWorkspace(d).bytes;
 }
 
 int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int64_t *cu_seqlens,
                          const int64_t *q_start, void *out, float *lse, int n_seq, int64_t total,
                          int H, int Hkv, int d, int64_t W, int n_sink, float scale, int zero_rest,
                          void *workspace, size_t workspace_bytes, void *stream) {
-  int e = paged_checks(n_seq, total, H, Hkv, d, W, n_sink, scale);
+  int e = chunk_paged_checks(n_seq, total, H, Hkv, d, W, n_sink, scale);
   if (e) return e;
   if (!q || !cu_seqlens || !q_start || !out || !aligned16(q) || !aligned16(out))
     return SWA_ERR_INVALID_ARG;
-  if (H / Hkv > 128) return SWA_ERR_UNSUPPORTED;
   swa::PagedFwdParams p = {};
   if ((e = paged_cache(cache, d, &p.c))) return e;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
@@ -1061,11 +1077,7 @@ int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache, const int6
   p.g_inv = ((1 << 16) + p.G - 1) / p.G;
   p.by_hkv = fast_div(Hkv);
   p.by_tu = fast_div(2 * p.tpt);
-  // A CTA walks empty entries of the unit list at about 10^7 a second while the others of
-  // its warps wait, a second at most.
-  if (static_cast<int64_t>(n_seq) * Hkv > kPagedMaxLists) return SWA_ERR_UNSUPPORTED;
-  const int64_t slots = (total / (2 * p.tpt) + n_seq) * Hkv;
-  if (slots > (1 << 30)) return SWA_ERR_UNSUPPORTED;
+  const int64_t slots = unit_slots(n_seq, total, H, Hkv);
   p.n_slots = static_cast<int>(slots);
   p.W = static_cast<int>(W < 0x7FFFFFFF - 1024 ? W : 0x7FFFFFFF - 1024);
   p.n_sink = n_sink;
@@ -1097,10 +1109,9 @@ int swa_attn_decode_paged(const void *q, const swa_paged_cache *cache, const int
                           void *out, float *lse, int B, int H, int Hkv, int d, int64_t W,
                           int n_sink, float scale, void *workspace, size_t workspace_bytes,
                           void *stream) {
-  int e = paged_checks(B, B, H, Hkv, d, W, n_sink, scale);
+  int e = decode_paged_checks(B, H, Hkv, d, W, n_sink, scale);
   if (e) return e;
   if (!q || !pos || !out || !aligned16(q) || !aligned16(out)) return SWA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(B) * H > (1 << 24)) return SWA_ERR_UNSUPPORTED;
   swa::PagedDecodeParams p = {};
   if ((e = paged_cache(cache, d, &p.c))) return e;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
