@@ -508,6 +508,15 @@ def _need_list(t, name, dtype, length):
                          f"{t.dtype} {list(t.shape)} on {t.device}")
 
 
+def _workspace_bytes(t):
+    """Size of a caller's workspace, whose elements must not share memory (as expanded ones do)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
+
+
 def _need_like(t, name, dtype, shape):
     _need(t, name, dtype, len(shape))
     if t.shape != shape:
@@ -662,6 +671,8 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
             == cu_seqlens.get_device() == q_start.get_device() == index):
         _elsewhere(index, k_cache=k_cache, v_cache=v_cache, block_table=block_table,
                    cu_seqlens=cu_seqlens, q_start=q_start)
+    if workspace is not None:
+        ws_bytes = _workspace_bytes(workspace)
     if not (new_out and lse is None and workspace is None):
         _elsewhere(index, out=out, lse=lse, workspace=workspace)
     # what is allocated here is zeroed by the call where no sequence writes, unless the other of
@@ -674,13 +685,13 @@ def swa_attn_chunk_paged(q, k_cache, v_cache, block_table, cu_seqlens, q_start, 
         if not zero_rest:
             lse.zero_()
     if workspace is None:
-        need = swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d)
-        workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
+        ws_bytes = max(swa_chunk_paged_workspace_bytes(n_seq, total, H, Hkv, d), 256)
+        workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
     check("swa_attn_chunk_paged",
           _on(index, lib().swa_attn_chunk_paged, q.data_ptr(), cache,
               cu_seqlens.data_ptr(), q_start.data_ptr(), out.data_ptr(), _ptr(lse), n_seq, total,
               H, Hkv, d, W, n_sink, scale, 1 if zero_rest else 0, workspace.data_ptr(),
-              workspace.numel() * workspace.element_size()))
+              ws_bytes))
     return (out, lse) if return_lse else out
 
 
@@ -715,6 +726,8 @@ def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
     if not (k_cache.get_device() == v_cache.get_device() == block_table.get_device()
             == pos.get_device() == index):
         _elsewhere(index, k_cache=k_cache, v_cache=v_cache, block_table=block_table, pos=pos)
+    if workspace is not None:
+        ws_bytes = _workspace_bytes(workspace)
     if not (out is None and lse is None and workspace is None):
         _elsewhere(index, out=out, lse=lse, workspace=workspace)
     if out is None:
@@ -722,12 +735,12 @@ def swa_attn_decode_paged(q, k_cache, v_cache, block_table, pos, W: int,
     if return_lse and lse is None:
         lse = q.new_empty((B, H), dtype=torch.float32)
     if workspace is None:
-        need = swa_decode_paged_workspace_bytes(B, H, Hkv, d)
-        workspace = q.new_empty(max(need, 256), dtype=torch.uint8)
+        ws_bytes = max(swa_decode_paged_workspace_bytes(B, H, Hkv, d), 256)
+        workspace = q.new_empty(ws_bytes, dtype=torch.uint8)
     check("swa_attn_decode_paged",
           _on(index, lib().swa_attn_decode_paged, q.data_ptr(), cache,
               pos.data_ptr(), out.data_ptr(), _ptr(lse), B, H, Hkv, d, W, n_sink, scale,
-              workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+              workspace.data_ptr(), ws_bytes))
     return (out, lse) if return_lse else out
 
 

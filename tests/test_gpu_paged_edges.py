@@ -224,3 +224,23 @@ def test_decode_weights_keep_32_bits(swa, pos, H, Hkv, d, page):
     tol -= (2.0 ** -8 - 2.0 ** -16) * mean_abs * (1 + 2.0 ** -8)
     check(to_f64(out), want, tol, "out")
     check(to_f64(lse), want_lse, tol_lse, "lse")
+
+
+def test_workspaces_that_share_memory_are_refused(swa):
+    """A workspace of enough elements that lie on one another, or not side by side."""
+    b = Batch([1] * 2, [5, 100], 4, 2, 64, 16, 64, 0)
+    need = max(swa.swa_chunk_paged_workspace_bytes(2, 2, 4, 2, 64),
+               swa.swa_decode_paged_workspace_bytes(2, 4, 2, 64))
+    one = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    for bad in (one[:1].expand(need), one.expand(need // 256 + 1, 256),
+                torch.zeros((need, 2), dtype=torch.uint8, device="cuda")[:, 0]):
+        for run in (run_chunk, run_decode):
+            with pytest.raises(ValueError):
+                run(swa, b, workspace=bad)
+    for run in (run_chunk, run_decode):
+        with pytest.raises(TypeError):
+            run(swa, b, workspace=need)
+    good = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for run in (run_chunk, run_decode):
+        out, lse = run(swa, b, workspace=good)
+        check_batch(b, out, lse.T if run is run_chunk else lse)
