@@ -508,8 +508,9 @@ typedef struct swa_rotation {
  *      v_new_stride elements apart (views of one fused projection work);
  *   q, q_out: [total, H, d] bf16, device, token rows q_stride and q_out_stride
  *      apart: the queries of the same tokens, rotated like the keys and
- *      written to q_out (q_out == q with equal strides rotates in place); or
- *      both NULL.  Strides: multiples of 8, at least heads * d.
+ *      written to q_out (q_out == q with equal strides rotates in place; what
+ *      is written must not overlap what is read in any other way); or both
+ *      NULL.  Strides: multiples of 8, at least heads * d.
  *   cu_seqlens: int64 [n_seq + 1], device: sequence b is tokens cu_seqlens[b]
  *      .. cu_seqlens[b+1] - 1, non-decreasing, cu_seqlens[n_seq] <= total.
  *   q_start: int64 [n_seq], device: the position of its first new token.
@@ -558,8 +559,12 @@ SWA_API size_t swa_decode_paged_workspace_bytes(int B, int H, int Hkv, int d);
  *   workspace: at least swa_chunk_paged_workspace_bytes(...) bytes, 256-byte
  *      aligned, caller-owned, contents on entry ignored; two calls in flight
  *      at once need workspaces of their own.
- * Values of visible slots must be finite; slots that no query of the call may
+ * Keys and values of visible slots must be finite.  (A row that sees a key
+ * whose score is NaN or +infinity is NaN; a value that is not finite reaches
+ * rows near it that do not see it, too.)  Slots that no query of the call may
  * see can hold anything, NaN and infinities included.
+ * The softmax weights are rounded to bf16 for the second matrix product, as
+ * in swa_attn_fwd; scores, maximum, sum and output are held in 32 bits.
  * SWA_ERR_DEVICE is set on the device for a sequence with offsets out of
  * range, a negative start or an end past max_pages * page_size (it is
  * skipped; the start of a sequence without tokens is not looked at), for
@@ -580,7 +585,9 @@ SWA_API int swa_attn_chunk_paged(const void *q, const swa_paged_cache *cache,
  * swa_attn_decode_paged -- batched single-token decode over a paged cache.
  * Passage: blog section 3.2; taxonomy page sections 1 (a decode step is bound
  * by reading the cache) and 3.2 (sinks).  The paged counterpart of
- * swa_attn_decode_ring, without a limit on H / Hkv.
+ * swa_attn_decode_ring, without a limit on H / Hkv; like there the weights
+ * are not rounded to 16 bits (they go into the matrix product as two bf16
+ * terms).  Keys and values are read once per 16 query heads that share them.
  *   q: [B, H, d] bf16, device: the query of sequence b at position pos[b],
  *      whose own key and value are in the cache; it reads key j iff
  *      j <= pos[b] and (j >= pos[b] - W + 1 or j < n_sink).

@@ -920,8 +920,10 @@ struct DecodePagedWorkspace {
   }
 };
 
-// Up to here a CTA per token is faster, beyond a warp per token (512 tokens 5.2 against
-// 7.3 us, 1024 tokens 9.3 against 8.2).
+// Up to here a CTA per token, beyond a warp per token.  Measured, CTA against warp, H / Hkv / d
+// = 32 / 8 / 128: 64 tokens 4.1 and 7.0 us, 768 tokens 6.0 and 8.1, 2048 tokens 11.5 and 11.5.
+// With fewer heads the CTA has less work per token and falls behind at the same place: 8 / 2 /
+// 64: 768 tokens 3.5 and 3.8, 2048 tokens 6.0 and 4.2; 4 / 1 / 64: 3.5 and 3.5, 6.0 and 3.8.
 constexpr int64_t kAppendFewTokens = 768;
 
 template <int D>

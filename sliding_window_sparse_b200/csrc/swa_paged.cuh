@@ -61,11 +61,11 @@ __device__ __forceinline__ int64_t mul_div(int64_t T, int c, int P) {
 // the latency of one counts.  Bound: bytes (every input row read once, every output
 // row written once), then, for few tokens, the chain of dependent loads offsets ->
 // start -> table entry; the token's first rows are loaded into registers before
-// that chain starts.  Measured with H = 32, Hkv = 8, d = 128: 64 tokens 3.9 us (a
-// warp each: 7.0), 512 tokens 5.2 (7.3), 1024 tokens 9.3 as CTAs and 8.2 as warps;
-// 9843 tokens 46 us (53 as CTAs), 5.3 TB/s; 16384 tokens with Hkv = 32 141 us, 5.7
-// TB/s.  Five items in flight per thread: with four the last takes 155 us, with six
-// (80 registers) 4096 tokens take 24 instead of 20 us.
+// that chain starts.  Measured with H = 32, Hkv = 8, d = 128: 64 tokens 4.1 us (a
+// warp each: 7.0), 768 tokens 6.0 (8.1), 2048 tokens 11.5 either way; 9843 tokens 47 us
+// (53 as CTAs), 5.1 TB/s; 16384 tokens with Hkv = 32 141 us, 5.7 TB/s.  Five items in
+// flight per thread: with four the last takes 155 us, with six (80 registers) 4096 tokens
+// take 24 instead of 20 us.
 //
 // The rotation of pair i turns (x, y) by a = position * inv_freq[i].  In 32
 // bits a would lose its fraction of a turn for far positions (position 10^5,

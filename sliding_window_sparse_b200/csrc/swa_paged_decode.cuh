@@ -1,7 +1,9 @@
 // swa_paged_decode.cuh -- batched single-token decode over a paged cache.
 //
-// The cost of a decode step is reading the visible keys and values once
-// (sparse-attention taxonomy page, section 1).  The work of a call is the list
+// The cost of a decode step is reading the visible keys and values
+// (sparse-attention taxonomy page, section 1): once for up to 16 query heads
+// per key/value head, ceil(G / 16) times for more, since a block of 16 heads is
+// a unit of its own.  The work of a call is the list
 // of 128-key tiles of every (sequence, key/value head, block of 16 query
 // heads); each CTA, one per SM, takes one contiguous run of that list, so all
 // of them stream the same number of bytes whatever the lengths are.  A unit
@@ -26,9 +28,12 @@
 // added in the end.  More heads take a second MMA per fragment (384 a tile).
 //
 // Measured (H / Hkv / d = 32 / 8 / 128): 64 sequences of 4096-key windows in pages of
-// 16 slots 172 us, 6.3 TB/s (a copy reaches 6.56); 24 sequences of up to 100000 keys with
-// 64 query heads in pages of 64 slots 773 us, 7.0 TB/s; one sequence of 1000 keys 8.6 us,
-// the latency of two launches, the page table, one tile and the merge (2.5 us).
+// 16 slots 171 us, 6.3 TB/s (a copy reaches 6.56); 24 sequences of up to 100000 keys with
+// 64 query heads in pages of 64 slots 757 us, 7.1 TB/s; one sequence of 1000 keys 8.8 us,
+// the latency of two launches, the page table, one tile and the merge (2.5 us).  The 64
+// sequences with 16 heads a group 181 us, with 20 330 and with 32 337; with d = 64 92 us in
+// pages of 64 slots, 5.8 TB/s, and 136 in pages of 16, whose boxes of 2 KB are bound by
+// the rate of TMA instructions.
 #pragma once
 #include <cstdint>
 #include <cuda.h>

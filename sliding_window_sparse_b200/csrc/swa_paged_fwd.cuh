@@ -13,9 +13,9 @@
 // cut into one run per CTA, so the SMs finish together whatever the lengths
 // are, and a few rows over a long context are spread over all SMs.  A unit
 // that a border cuts leaves unnormalised rows (output, running maximum and
-// sum) that paged_fwd_merge_kernel joins.  Short units are not cut (keep_whole).  Units are listed column by column of
-// a matrix with one column per CTA, so CTAs that run at the same time read
-// neighbouring windows, which L2 holds.
+// sum) that paged_fwd_merge_kernel joins.  Short units are not cut (keep_whole).
+// Units are listed column by column of a matrix with one column per CTA, so CTAs that run
+// at the same time read neighbouring windows, which L2 holds.
 //
 // Roles (384 threads):
 //   warp 0    producer: Q_A, Q_B, then K and V tiles into their rings; lane i
@@ -44,9 +44,11 @@
 //
 // Bound: the chain S -> softmax -> PV of a tile, 1.6 us for both query tiles, where the
 // MMAs and the exponentials of a step (2048 cycles each) would allow 1.1.  Measured with
-// H / Hkv / d = 32 / 8 / 128: a prompt of 8192 tokens 440 us, 1250 TFLOP/s; 4 x 512 tokens
-// over full 4096-key windows 134 us, 1025; 61 tokens over 130000 keys 132 us; five drafted
-// tokens over 1000 keys (8 / 2 / 64) 10.8 us.  Behind the last tile the merge takes 10.6 us
+// H / Hkv / d = 32 / 8 / 128: a prompt of 8192 tokens 443 us, 1240 TFLOP/s; 4 x 512 tokens
+// over full 4096-key windows 134 us, 1025 (pages of 16 slots; 128 of 64 or more, 185 of 8, where a
+// key tile takes 64 TMA instructions of 1 KB); 61 tokens over 130000 keys 129 us; five drafted
+// tokens over 1000 keys (8 / 2 / 64) 11.2 us.  With d = 64 half the MMA work meets the same
+// softmax: 4 x 512 tokens 109 us, the prompt 373.  Behind the last tile the merge takes 10.6 us
 // where all borders cut a unit and 3 us where none does; a unit's start and epilogue cost
 // about 5 us of its SM.
 #pragma once
@@ -61,7 +63,10 @@
 
 namespace swa {
 
-constexpr int kUnitCost = 1;   // of a unit besides its key tiles, in key tiles
+// Of a unit besides its key tiles, in key tiles.  (A start and epilogue take three tiles' time,
+// but 2 and 3 measured like 1: within 1% on prompts, chunks and narrow windows, 2 to 4% either
+// way on ragged batches.)
+constexpr int kUnitCost = 1;
 constexpr int kUnitRing = 4;   // units the scheduler is ahead
 
 // n / d for n < 2^31 by a multiplication: mul = ceil(2^(31 + l) / d), l = ceil(log2 d),
@@ -205,15 +210,19 @@ __device__ __forceinline__ int paged_unit(const PagedFwdParams &p, int u, PagedU
 }
 
 // Whether a unit goes whole to the run in which it starts.  Cutting it balances the runs
-// to a tile, but the parts of 148 cut units cost about 10 us (77 MB of partials written and
-// read back, most of it behind the last tile), some 6 key tiles of an SM.  With units of
-// equal cost the longest run exceeds T / P by the remainder to a whole unit.  Measured, cut
-// against whole, one sequence with 32 own key/value heads (excess in tiles): window 512,
-// 8191 tokens (3) 125 and 117 us, 4096 tokens (5) 72 and 68; window 128, 2047 tokens (2) 34
-// and 28; window 1024, 8191 tokens (5) 163 and 158, 2047 tokens (7) 50 and 51, 4096 tokens
-// (10) 88 and 93.  Long units differ in cost, so that a run may end up far above the mean
-// (window 2048: 235 and 244), and where a run is a tile or two (ten drafted tokens) cutting
-// wins 11 us against 16: few parts are joined in 3 us.
+// to a tile, but the parts of 148 cut units cost about 10 us (39 MB of partials written by
+// this kernel and read by the merge, most of it behind the last tile), some 6 key tiles of an
+// SM.  With units of equal cost the longest run exceeds T / P by the remainder to a whole
+// unit.  Measured, cut against whole, one sequence with 32 own key/value heads (excess in
+// tiles): window 512, 8191 tokens (3) 124 and 116 us, 4096 tokens (5) 70.5 and 69.3; window
+// 128, 2047 tokens (2) 34 and 29; window 1024, 8191 tokens (5) 164 and 161.  Where a run is a
+// tile or two (ten drafted tokens) cutting wins 11 us against 16: few parts are joined in 3 us.
+//
+// For units of unlike cost this is a prediction only: over 1000 random ragged batches that
+// the rule takes (simulated), the longest run is more than 6 tiles above T / P in 25%, 12 at
+// worst.  Measured, cut against whole, 32 sequences of 1 to 512 tokens with 32 and 8 own
+// key/value heads: window 256 138 and 136 us, 100 and 101; window 512 168 and 170, 117 and
+// 116; window 1024 228 and 237, 156 and 163.
 constexpr int kWholeCost = 12, kWholeExcess = 6, kWholeRun = 3;
 __device__ __forceinline__ bool keep_whole(int64_t T, int P, int most) {
   if (most > kWholeCost || T < kWholeRun * P || T >= (int64_t(1) << 31) || T == 0) return false;
